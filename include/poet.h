@@ -418,6 +418,142 @@ POET_API poet_status poet_llama_block_backward(const poet_llama_block *blk, cons
                                                int64_t T, void *dh, float *const *G, void *ws, size_t ws_bytes,
                                                poet_stream stream);
 
+/* ---------------------------------------------------------------- the joint between two blocks (adjacent)
+ *
+ * What joins a block's output to the residual stream and the stream to the
+ * next block, in one pass: the norm after a block, its gate and residual
+ * scale, and the norm before the next block.  For token t, with the branch's
+ * output o, the stream h and the gate g of the token:
+ *   p  = o / sqrt(mean(o^2) + eps) * w_post      (post_norm; otherwise p = o)
+ *   h' = alpha h + beta act(g) p                 (act(g) = 1 without a gate)
+ *   n  = h' / sqrt(mean(h'^2) + eps) * w_pre     (if n is wanted)
+ * The norms are the block's RMSNorm (eps inside the square root) with trained
+ * gains.  Sums are float; n is formed from h' before h' is rounded. */
+typedef enum { POET_GATE_NONE = 0, POET_GATE_CHANNEL = 1, POET_GATE_ROW = 2 } poet_gate;
+typedef enum { POET_GATE_LINEAR = 0, POET_GATE_SIGMOID = 1 } poet_gate_act;
+
+typedef struct {
+  int32_t d;           /* width of the stream, 1 <= d <= 16384 */
+  int32_t dtype;       /* poet_dtype of o, h, h', n, the gate and their gradients */
+  int32_t post_norm;   /* 1: normalize o (w_post); 0: use it as it is */
+  int32_t gate;        /* poet_gate: none, one value per channel (G x d), or one value (G) */
+  int32_t gate_act;    /* poet_gate_act applied to the gate's values */
+  int32_t reserved;    /* 0 */
+  int64_t gate_rows;   /* consecutive tokens that share one gate row, >= 1: token t takes row
+                          t / gate_rows of G = ceil(T / gate_rows) (1: a gate of its own for
+                          each token; T: one gate for all) */
+  float alpha, beta;   /* scale of the stream and of the branch (finite) */
+  float eps;           /* > 0 */
+  const float *w_post; /* device float[d], gains of the norm after the block (NULL: 1) */
+  const float *w_pre;  /* device float[d], gains of the norm before the next block (NULL: 1) */
+} poet_joint;
+
+/* o, h: device T x d, row strides ldo, ldh (elements, >= d); gate: device G x d
+ * with row stride ldg >= d, or G values at stride ldg >= 1 (NULL without a
+ * gate).  Writes h_out = h' and n (row strides ldho, ldn); n may be NULL (no
+ * norm before the next block).  o may be NULL: then h' = h (alpha, beta, gate
+ * and post_norm do not apply, h_out must be NULL) and the call is the norm
+ * before the first block.  h_out may be h, and n or h_out may be o (the same
+ * address and stride).  Any strides and element-aligned addresses are taken;
+ * rows that all start on 16 bytes are moved in 16-byte units. */
+POET_API poet_status poet_joint_forward(const poet_joint *J, const void *o, int64_t ldo, const void *h, int64_t ldh,
+                                        const void *gate, int64_t ldg, int64_t T, void *h_out, int64_t ldho, void *n,
+                                        int64_t ldn, poet_stream stream);
+
+/* Bytes of workspace poet_joint_backward needs (0 if J or T is invalid). */
+POET_API size_t poet_joint_workspace_bytes(const poet_joint *J, int64_t T);
+
+/* For the gradients dh_out of h' and dn of n (either may be NULL: no gradient
+ * reaches the joint there), writes dh (of h), d_o (of o), dgate (of the gate:
+ * same shape and element type, row stride lddg; summed over the tokens that
+ * share a row) and dw_post, dw_pre (device float[d], overwritten).  o, h_out,
+ * gate: the forward's input, output and gate (h_out = h when o is NULL; then
+ * d_o, dgate and dw_post must be NULL).  dgate, dw_post and dw_pre may be NULL
+ * when they are not wanted; h_out may be NULL when dn is.  dh may be dh_out or
+ * dn, d_o may be o (the same address and stride).  Sums run in a fixed order: the
+ * same inputs give the same bits.  ws: device, poet_joint_workspace_bytes,
+ * 256-byte aligned.  T = 0: dw_post and dw_pre are zeroed. */
+POET_API poet_status poet_joint_backward(const poet_joint *J, const void *o, int64_t ldo, const void *h_out,
+                                         int64_t ldho, const void *gate, int64_t ldg, const void *dh_out,
+                                         int64_t lddho, const void *dn, int64_t lddn, int64_t T, void *dh,
+                                         int64_t lddh, void *d_o, int64_t lddo, void *dgate, int64_t lddg,
+                                         float *dw_post, float *dw_pre, void *ws, size_t ws_bytes,
+                                         poet_stream stream);
+
+/* ---------------------------------------------------------------- log probabilities and losses on logits (adjacent)
+ *
+ * What a training or validation step does with the logits behind the last
+ * block.  The pages report validation perplexity ([P1] Key results), which is
+ * exp(-mean logp) of poet_token_logprobs; they fix no loss.
+ *  - logits: device T x V (dtype), row stride ld >= V elements, element-aligned;
+ *    1 <= V <= 2097152.  Only the V columns of a row are read.  The
+ *    distribution of a row is p_v = softmax(scale x_v), scale > 0 (an inverse
+ *    temperature).
+ *  - A logit of -inf is a masked token: its probability and its gradient are 0
+ *    and it is never listed as an alternative.  A row of nothing but -inf has
+ *    log probability -inf, entropy 0 and a gradient of 0.  A row with a NaN or
+ *    +inf logit gives NaN (and no alternatives) for that row alone.
+ *  - tokens: device int32[T].  A negative token marks a row to leave out
+ *    (padding): its logits are not read, its log probability, entropy and
+ *    gradient are 0 and its alternatives empty.  A token >= V does the same and
+ *    is reported by poet_sync_status (POET_EBOUNDS).
+ *  - saved: device float[4 T], 16-byte aligned, row t: {the row's largest
+ *    logit M, ln sum exp(scale (x - M)), the entropy, ln of the same sum over
+ *    the tokens outside the teacher's}.  The third is poet_token_logprobs's,
+ *    the fourth poet_distill_topk's (tail); a call writes 0 in what is not its
+ *    own.  It is what the backward reads.
+ *  - Sums are float and run in a fixed order. */
+
+/* logp[t] = ln p of tokens[t]; entropy[t] = -sum p ln p; top_tokens, top_logp
+ * (T x topk, 0 <= topk <= 128): the topk most likely tokens of the row in
+ * falling order (equal logits: the lower token first) and their log
+ * probabilities; entries beyond the row's unmasked tokens are -1 and -inf.
+ * tokens may be NULL (then logp must be; every row is taken); any output may
+ * be NULL (top_tokens and top_logp together, when topk is 0). */
+POET_API poet_status poet_token_logprobs(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                                         float scale, const int32_t *tokens, int32_t topk, float *logp,
+                                         float *entropy, int32_t *top_tokens, float *top_logp, float *saved,
+                                         poet_stream stream);
+
+/* dlogits (T x V, dtype, row stride ldd) = the gradient of
+ * sum_t dlogp[t] logp[t] + dentropy[t] entropy[t]:
+ *   scale (dlogp (1[v = token] - p_v) - dentropy p_v (ln p_v + entropy)).
+ * dlogp, dentropy: device float[T], either may be NULL; tokens may be NULL when
+ * dlogp is.  saved: the forward's.  dlogits may be logits (the same stride).
+ * With dlogp = -1/T this is the gradient of the cross-entropy loss. */
+POET_API poet_status poet_token_logprobs_grad(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                                              float scale, const int32_t *tokens, const float *saved,
+                                              const float *dlogp, const float *dentropy, void *dlogits, int64_t ldd,
+                                              poet_stream stream);
+
+/* Distillation from a teacher's top logits.  Row t has K entries (1 <= K <=
+ * 128): teacher_tokens int32 and teacher_values float (device T x K,
+ * contiguous); an entry with a negative token is left out (rows may have fewer
+ * than K), one >= V too (reported as POET_EBOUNDS); a row with no entry left
+ * has loss and gradient 0 and its logits are not read.  With u = value_scale * value:
+ *   tail = 0: q = softmax(u) over the entries,
+ *             loss = sum_k q_k (ln q_k - ln p_k);
+ *   tail = 1: u are log probabilities (poet_token_logprobs's top_logp), q = exp(u),
+ *             q_r = max(0, 1 - sum q) is the teacher's mass on all other
+ *             tokens and p_r the student's:
+ *             loss = sum_k q_k (ln q_k - ln p_k) + q_r (ln q_r - ln p_r).
+ *             What is left below 2^-23 per entry is rounding and counts as 0.
+ * A value of -inf has q = 0.  A token listed twice counts with both values.
+ * loss: device float[T].  dlogits (may be NULL; T x V, dtype, row stride ldd,
+ * may be logits): the gradient of sum_t dloss[t] loss[t] (dloss: device
+ * float[T], NULL = 1).  K = 1, tail = 0 is the cross-entropy loss of given
+ * tokens with its gradient in one call. */
+POET_API poet_status poet_distill_topk(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                                       float scale, const int32_t *teacher_tokens, const float *teacher_values,
+                                       int32_t K, float value_scale, int32_t tail, const float *dloss, float *loss,
+                                       float *saved, void *dlogits, int64_t ldd, poet_stream stream);
+
+/* The gradient alone, from the forward's saved. */
+POET_API poet_status poet_distill_topk_grad(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                                            float scale, const int32_t *teacher_tokens, const float *teacher_values,
+                                            int32_t K, float value_scale, int32_t tail, const float *saved,
+                                            const float *dloss, void *dlogits, int64_t ldd, poet_stream stream);
+
 /* ---------------------------------------------------------------- utilities */
 
 /* Batched dense product on the library's GEMM engine, exported so that the

@@ -15,6 +15,8 @@ import torch
 F32, BF16 = 0, 1
 BS, FS = 0, 1
 PLAN_AUTO, PLAN_TOKEN, PLAN_WEIGHT = 0, 1, 2
+GATE_NONE, GATE_CHANNEL, GATE_ROW = 0, 1, 2
+GATE_LINEAR, GATE_SIGMOID = 0, 1
 OK, EINVAL, ECUDA, ETIMEOUT, ENOMEM_WS, EBOUNDS = 0, 1, 2, 3, 4, 5
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpoet.so")
@@ -42,6 +44,13 @@ class poet_layer(ctypes.Structure):
 class poet_llama_block(ctypes.Structure):
     _fields_ = [("seq_len", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("rope_base", ctypes.c_float), ("norm_eps", ctypes.c_float), ("lin", poet_layer * 7)]
+
+
+class poet_joint(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("gate_act", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("gate_rows", ctypes.c_int64), ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("eps", ctypes.c_float), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p)]
 
 
 class poet_adamw_hparams(ctypes.Structure):
@@ -122,6 +131,26 @@ _SIGS = {
     "poet_llama_block_backward": (ctypes.c_int, [ctypes.POINTER(poet_llama_block), ctypes.c_void_p, ctypes.c_void_p,
                                                  ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                  ctypes.c_size_t, ctypes.c_void_p]),
+    "poet_joint_forward": (ctypes.c_int, [ctypes.POINTER(poet_joint)] + [ctypes.c_void_p, ctypes.c_int64] * 3 +
+                           [ctypes.c_int64] + [ctypes.c_void_p, ctypes.c_int64] * 2 + [ctypes.c_void_p]),
+    "poet_joint_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(poet_joint), ctypes.c_int64]),
+    "poet_joint_backward": (ctypes.c_int, [ctypes.POINTER(poet_joint)] + [ctypes.c_void_p, ctypes.c_int64] * 5 +
+                            [ctypes.c_int64] + [ctypes.c_void_p, ctypes.c_int64] * 3 +
+                            [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "poet_token_logprobs": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                           ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32] +
+                            [ctypes.c_void_p] * 6),
+    "poet_token_logprobs_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                                ctypes.c_int32, ctypes.c_float] + [ctypes.c_void_p] * 5 +
+                                 [ctypes.c_int64, ctypes.c_void_p]),
+    "poet_distill_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                         ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_int32, ctypes.c_float, ctypes.c_int32] + [ctypes.c_void_p] * 4 +
+                          [ctypes.c_int64, ctypes.c_void_p]),
+    "poet_distill_topk_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                              ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_float, ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                               [ctypes.c_int64, ctypes.c_void_p]),
     "poet_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_void_p]),
     "poet_adamw_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_float,
@@ -636,3 +665,238 @@ class PoetBlock:
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=self.layers[0].W0.device)
         cayley_neumann_grad_many(self.layers, G, dth, ws, stream)
         return dth
+
+
+# ------------------------------------------------------------------ the joint between two blocks
+
+def _dtype_of(t, what):
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+
+
+def _operand(t, name, shape, dtype, device, rows=True):
+    """A device operand: its address and row stride (rows contiguous), after checks."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if rows and t.dim() == 2:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"the rows of {name} must be contiguous (stride(1) == 1)")
+        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), 1
+
+
+def _current(t, name):
+    """The library launches on the current device: operands must be there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+_MAXI32 = 2**31 - 1
+
+
+def _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps):
+    """The poet_joint of these options, with the addresses and strides of o, h and the gate."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D (tokens x width)")
+    dev = _current(h, "h")
+    T, d = h.shape
+    J = poet_joint(min(d, _MAXI32), _dtype_of(h, "h"), 1 if post_norm and o is not None else 0, GATE_NONE, gate_act, 0,
+                   gate_rows, alpha, beta, eps, None, None)
+    ph = _operand(h, "h", (T, d), h.dtype, dev)
+    po = (None, 0)
+    pg = (None, 0)
+    if o is not None:
+        po = _operand(o, "o", (T, d), h.dtype, dev)
+        if w_post is not None:
+            J.w_post = _operand(w_post, "w_post", (d,), torch.float32, dev)[0]
+        if gate is not None:
+            if gate_rows < 1:
+                raise ValueError("gate_rows must be at least 1")
+            G = -(-T // gate_rows)
+            J.gate = GATE_CHANNEL if gate.dim() == 2 else GATE_ROW
+            if gate.dim() == 1:
+                pg = (_operand(gate, "gate", (G,), h.dtype, dev, rows=False)[0], 1)
+            else:
+                pg = _operand(gate, "gate", (G, d), h.dtype, dev)
+    elif gate is not None or w_post is not None:
+        raise ValueError("a gate and w_post need o")
+    if w_pre is not None:
+        J.w_pre = _operand(w_pre, "w_pre", (d,), torch.float32, dev)[0]
+    return J, dev, T, d, po, ph, pg
+
+
+def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, pre_norm=True, gate_act=GATE_LINEAR,
+                  gate_rows=1, alpha=1.0, beta=1.0, eps=1e-6, h_out=None, n=None, stream=None):
+    """(h', n): h' = alpha h + beta act(gate) rmsnorm(o) w_post, n = rmsnorm(h') w_pre (poet_joint_forward).
+
+    o, h: T x d (float32 or bfloat16, rows contiguous).  gate: G x d or G values, G = ceil(T / gate_rows),
+    shared by gate_rows consecutive tokens.  w_post, w_pre: float32 [d] or None (gains of 1).  post_norm=False
+    takes o as it is; pre_norm=False leaves n out (None).  o=None: n = rmsnorm(h) w_pre alone (h' is None).
+    h_out and n are allocated where they are not given."""
+    J, dev, T, d, po, ph, pg = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps)
+    if o is None and (h_out is not None or not pre_norm):
+        raise ValueError("without o there is only n")
+    if o is not None and h_out is None:
+        h_out = torch.empty(T, d, dtype=h.dtype, device=dev)
+    if not pre_norm and (n is not None or w_pre is not None):
+        raise ValueError("n and w_pre need pre_norm")
+    if pre_norm and n is None:
+        n = torch.empty(T, d, dtype=h.dtype, device=dev)
+    pho = _operand(h_out, "h_out", (T, d), h.dtype, dev) if o is not None else (None, 0)
+    pn = _operand(n, "n", (T, d), h.dtype, dev) if pre_norm else (None, 0)
+    _check(lib().poet_joint_forward(ctypes.byref(J), *po, *ph, *pg, T, *pho, *pn, _stream(stream)))
+    return h_out, n
+
+
+def joint_workspace_bytes(T, d, dtype, gate=GATE_NONE, gate_rows=1):
+    """Bytes of workspace joint_backward needs (dtype: F32 or BF16)."""
+    J = poet_joint(d, dtype, 0, gate, 0, 0, gate_rows, 1.0, 1.0, 1.0, None, None)
+    return lib().poet_joint_workspace_bytes(ctypes.byref(J), T)
+
+
+def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_norm=True, gate_act=GATE_LINEAR,
+                   gate_rows=1, alpha=1.0, beta=1.0, eps=1e-6, dh=None, d_o=None, dgate=None, dw_post=None,
+                   dw_pre=None, ws=None, stream=None):
+    """(dh, d_o, dgate, dw_post, dw_pre) of joint_forward for the gradients dh_out of h' and dn of n (either may
+    be None).  o, gate and the options are the forward's, h_out its result (h where o is None).  Gradients of
+    what the joint does not have are None; the others are allocated where they are not given (ws too)."""
+    J, dev, T, d, po, ph, pg = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps)
+    t = h_out.dtype
+    if dn is None and w_pre is not None:
+        raise ValueError("w_pre needs dn")
+    pd = _operand(dh_out, "dh_out", (T, d), t, dev) if dh_out is not None else (None, 0)
+    pn = _operand(dn, "dn", (T, d), t, dev) if dn is not None else (None, 0)
+    if dh is None:
+        dh = torch.empty(T, d, dtype=t, device=dev)
+    if o is not None and d_o is None:
+        d_o = torch.empty(T, d, dtype=t, device=dev)
+    if gate is not None and dgate is None:
+        dgate = torch.empty(gate.shape, dtype=t, device=dev)
+    if w_post is not None and dw_post is None:
+        dw_post = torch.empty(d, dtype=torch.float32, device=dev)
+    if w_pre is not None and dw_pre is None:
+        dw_pre = torch.empty(d, dtype=torch.float32, device=dev)
+    for name, have, want in (("d_o", d_o, o), ("dgate", dgate, gate), ("dw_post", dw_post, w_post),
+                             ("dw_pre", dw_pre, w_pre)):
+        if have is not None and want is None:
+            raise ValueError(f"{name} is the gradient of something this joint does not have")
+    pdh = _operand(dh, "dh", (T, d), t, dev)
+    pdo = _operand(d_o, "d_o", (T, d), t, dev) if d_o is not None else (None, 0)
+    pdg = (None, 0)
+    if dgate is not None:
+        pdg = _operand(dgate, "dgate", gate.shape, t, dev, rows=gate.dim() == 2)
+    pwq = _operand(dw_post, "dw_post", (d,), torch.float32, dev)[0] if dw_post is not None else None
+    pwn = _operand(dw_pre, "dw_pre", (d,), torch.float32, dev)[0] if dw_pre is not None else None
+    if ws is None:
+        ws = torch.empty(max(lib().poet_joint_workspace_bytes(ctypes.byref(J), T), 1), dtype=torch.uint8, device=dev)
+    _check(lib().poet_joint_backward(ctypes.byref(J), *po, *ph, *pg, *pd, *pn, T, *pdh, *pdo, *pdg, pwq, pwn,
+                                     _ptr(ws), ws.numel(), _stream(stream)))
+    return dh, d_o, dgate, dw_post, dw_pre
+
+
+# ------------------------------------------------------------------ log probabilities and losses on logits
+
+def _logits(x, name="logits"):
+    """(device, dtype, T, V, address, row stride) of a matrix of logits."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (tokens x vocabulary)")
+    dev = _current(x, name)
+    T, V = x.shape
+    return (dev, _dtype_of(x, name), T, min(V, _MAXI32)) + _operand(x, name, (T, V), x.dtype, dev)
+
+
+def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, saved=None, stream=None):
+    """(logp, entropy, top_tokens, top_logp, saved) of each row of logits (poet_token_logprobs).
+
+    tokens: int32 [T] or None (then logp is None); a negative token leaves its row out.  topk: how many
+    alternatives to list (0: none).  entropy=False leaves the entropy out (None).  saved: float32 [T, 4],
+    what token_logprobs_grad reads (allocated where it is not given)."""
+    dev, dt, T, V, px, ld = _logits(logits)
+    logp = pt = None
+    if tokens is not None:
+        pt = _operand(tokens, "tokens", (T,), torch.int32, dev, rows=False)[0]
+        logp = torch.empty(T, dtype=torch.float32, device=dev)
+    H = torch.empty(T, dtype=torch.float32, device=dev) if entropy else None
+    top = topl = None
+    if topk > 0:
+        top = torch.empty(T, topk, dtype=torch.int32, device=dev)
+        topl = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    if saved is None:
+        saved = torch.empty(T, 4, dtype=torch.float32, device=dev)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
+    _check(lib().poet_token_logprobs(px, ld, dt, T, V, scale, pt, topk, _ptr(logp), _ptr(H), _ptr(top), _ptr(topl), ps,
+                                     _stream(stream)))
+    return logp, H, top, topl, saved
+
+
+def token_logprobs_grad(logits, tokens, saved, dlogp=None, dentropy=None, *, scale=1.0, dlogits=None, stream=None):
+    """dlogits for the gradients dlogp and dentropy (float32 [T], either may be None) of token_logprobs's
+    results; saved: the forward's (with its entropy where dentropy is given).  dlogits may be logits."""
+    dev, dt, T, V, px, ld = _logits(logits)
+    pt = _operand(tokens, "tokens", (T,), torch.int32, dev, rows=False)[0] if tokens is not None else None
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
+    pl = _operand(dlogp, "dlogp", (T,), torch.float32, dev, rows=False)[0] if dlogp is not None else None
+    pe = _operand(dentropy, "dentropy", (T,), torch.float32, dev, rows=False)[0] if dentropy is not None else None
+    if dlogits is None:
+        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev)
+    _check(lib().poet_token_logprobs_grad(px, ld, dt, T, V, scale, pt, ps, pl, pe, pd, ldd, _stream(stream)))
+    return dlogits
+
+
+def _teacher(teacher_tokens, teacher_values, T, dev):
+    if teacher_tokens.dim() != 2:
+        raise ValueError("teacher_tokens must be 2-D (tokens x entries)")
+    K = teacher_tokens.shape[1]
+    return (_operand(teacher_tokens, "teacher_tokens", (T, K), torch.int32, dev, rows=False)[0],
+            _operand(teacher_values, "teacher_values", (T, K), torch.float32, dev, rows=False)[0], min(K, _MAXI32))
+
+
+def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tail=False, scale=1.0, dloss=None,
+                 grad=False, dlogits=None, saved=None, stream=None):
+    """(loss, dlogits, saved) of each row of logits against a teacher's top logits (poet_distill_topk).
+
+    teacher_tokens: int32 [T, K], negative entries left out; teacher_values: float32 [T, K], logits
+    (tail=False: renormalized over the entries) or log probabilities (tail=True: what they leave of the mass
+    is one more outcome).  grad=True (or dlogits given): dlogits is the gradient of sum dloss * loss (dloss:
+    float32 [T], None = 1), formed in the same pass; otherwise None.  dlogits may be logits."""
+    dev, dt, T, V, px, ld = _logits(logits)
+    pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
+    pw = _operand(dloss, "dloss", (T,), torch.float32, dev, rows=False)[0] if dloss is not None else None
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    if saved is None:
+        saved = torch.empty(T, 4, dtype=torch.float32, device=dev)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
+    if grad and dlogits is None:
+        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev) if dlogits is not None else (None, 0)
+    _check(lib().poet_distill_topk(px, ld, dt, T, V, scale, pt, pv, K, value_scale, 1 if tail else 0, pw,
+                                   loss.data_ptr(), ps, pd, ldd, _stream(stream)))
+    return loss, dlogits, saved
+
+
+def distill_topk_grad(logits, teacher_tokens, teacher_values, saved, dloss=None, *, value_scale=1.0, tail=False,
+                      scale=1.0, dlogits=None, stream=None):
+    """dlogits = the gradient of sum dloss * loss, from the forward's saved.  dlogits may be logits."""
+    dev, dt, T, V, px, ld = _logits(logits)
+    pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
+    pw = _operand(dloss, "dloss", (T,), torch.float32, dev, rows=False)[0] if dloss is not None else None
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
+    if dlogits is None:
+        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev)
+    _check(lib().poet_distill_topk_grad(px, ld, dt, T, V, scale, pt, pv, K, value_scale, 1 if tail else 0, ps, pw, pd,
+                                        ldd, _stream(stream)))
+    return dlogits
