@@ -26,6 +26,10 @@ namespace {
 
 constexpr int MAX_D = 16384;
 
+// How the kernels are specialized by the gate: none or one value per row, a
+// channel gate of every row's own, a channel gate shared by rows.
+enum { GK_ROW = 0, GK_EACH = 1, GK_SHARED = 2 };
+
 struct JointFwdArgs {
   const void *o, *h, *gate;
   void *h_out, *n;
@@ -37,7 +41,46 @@ struct JointFwdArgs {
   float alpha, beta, eps;
 };
 
-__device__ __forceinline__ float act_of(float g, int sig) { return sig ? 1.f / (1.f + expf(-g)) : g; }
+// The sigmoid's exponential and quotient are the fast ones: their few units in
+// the last place are far below an output's rounding.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+__device__ __forceinline__ float act_of(float g, int sig) { return sig ? sigmoid(g) : g; }
+
+// A thread's own ring of the rows to come.  With S stages every thread copies
+// its 16 bytes of each operand of row r + S - 1 into its own place in shared
+// memory (cp.async) while it works on row r, and only it reads them: no barrier
+// is needed and S - 1 rows are in flight without holding registers.  S = 0:
+// rows are read when they are needed, the next one ahead in registers.
+template <int S, int NV>
+struct Ring {
+  uint32_t base;
+  int stride, stage;  // bytes from one vector of a thread to its next, of one stage
+  __device__ __forceinline__ void init(int operands) {
+    extern __shared__ __align__(16) unsigned char joint_smem[];
+    base = uint32_t(__cvta_generic_to_shared(joint_smem)) + threadIdx.x * 16;
+    stride = blockDim.x * 16;
+    stage = stride * NV * operands;
+  }
+  // The places of a thread beyond the row's end hold zeros.
+  __device__ __forceinline__ void zero(int stages) const {
+    for (uint32_t p = base; p < base + stages * stage; p += stride)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ uint32_t at(int s, int operand, int j) const {
+    return base + s * stage + (operand * NV + j) * stride;
+  }
+  static __device__ __forceinline__ void copy(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S >= 2 ? S - 2 : 0) : "memory"); }
+  template <typename V>
+  static __device__ __forceinline__ void read(V &v, uint32_t src) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(src));
+    if constexpr (sizeof(V) == 16) v = *reinterpret_cast<const V *>(&r);
+  }
+};
 
 // The row groups of a CTA: `tpr` threads (whole warps) each.
 struct Group {
@@ -53,115 +96,239 @@ struct Group {
   }
 };
 
-template <typename T, int VW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) joint_fwd_kernel(const JointFwdArgs a) {
-  __shared__ float red[8][2][32];
+// The elements of a row that a thread holds, as read: NV vectors of VW
+// elements, tpr vectors apart, zero beyond the row's end (where nothing is ever
+// loaded).  Their values come in pairs: the arithmetic is two floats an
+// instruction, because the kernels issue close to one instruction a cycle.
+template <typename T, int VW, int NV>
+struct Lane {
+  static constexpr int N = VW * NV, NP = N / 2;
+  RowVec<T, VW> v[NV];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = RowVec<T, VW>{};
+  }
+  __device__ __forceinline__ void get(float2 (&x)[NP]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[VW];
+      v[j].get(f);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) (((j * VW + e) & 1) ? x[(j * VW + e) / 2].y : x[(j * VW + e) / 2].x) = f[e];
+    }
+  }
+  static __device__ __forceinline__ void put(T *row, int tid, int tpr, int d, const float2 (&x)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (tid + j * tpr) * VW;
+      float f[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) f[e] = ((j * VW + e) & 1) ? x[(j * VW + e) / 2].y : x[(j * VW + e) / 2].x;
+      if (c < d) RowVec<T, VW>::store(row + c, f);
+    }
+  }
+};
+
+// The same elements of a float vector of the row's width: gains, column sums.
+template <int VW, int NV>
+__device__ __forceinline__ void gains(float2 (&w)[VW * NV / 2], const float *p, int tid, int tpr, int d) {
+#pragma unroll
+  for (int i = 0; i < VW * NV; ++i) {
+    const int c = (tid + i / VW * tpr) * VW + i % VW;
+    const float f = p && c < d ? p[c] : 1.f;
+    ((i & 1) ? w[i / 2].y : w[i / 2].x) = f;
+  }
+}
+// The gains in the backward: of the ring's variants in shared memory, behind the
+// ring, every thread's own (no barrier), because the column sums need the
+// registers; of the others in registers.
+template <int VW, int NV, bool SMEM>
+struct Gains {
+  static constexpr int NP = VW * NV / 2;
+  float2 w[SMEM ? 1 : NP];
+  uint32_t at;
+  __device__ __forceinline__ void init(const float *p, uint32_t base, int tid, int tpr, int d) {
+    if constexpr (SMEM) {
+      float2 f[NP];
+      gains<VW, NV>(f, p, tid, tpr, d);
+      at = base + threadIdx.x * 16;
+#pragma unroll
+      for (int i = 0; i < NP; i += 2)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + i / 2 * blockDim.x * 16), "f"(f[i].x),
+                     "f"(f[i].y), "f"(f[i + 1].x), "f"(f[i + 1].y)
+                     : "memory");
+    } else {
+      gains<VW, NV>(w, p, tid, tpr, d);
+    }
+  }
+  __device__ __forceinline__ void get(float2 (&f)[NP]) const {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (SMEM) {
+        if (i % 2 == 0)
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(f[i].x), "=f"(f[i].y), "=f"(f[i + 1].x), "=f"(f[i + 1].y)
+                       : "r"(at + i / 2 * blockDim.x * 16));
+      } else {
+        f[i] = w[i];
+      }
+    }
+  }
+};
+template <int VW, int NV>
+__device__ __forceinline__ void put_floats(float *p, int tid, int tpr, int d, const float2 (&x)[VW * NV / 2]) {
+#pragma unroll
+  for (int i = 0; i < VW * NV; ++i) {
+    const int c = (tid + i / VW * tpr) * VW + i % VW;
+    if (c < d) p[c] = (i & 1) ? x[i / 2].y : x[i / 2].x;
+  }
+}
+
+__device__ __forceinline__ void zero_slots(float *p, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0.f;
+  __syncthreads();
+}
+
+template <typename T, int VW, int NV, int S, int GK, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArgs a) {
+  __shared__ __align__(16) float red[8][2][32];
+  zero_slots(red[0][0], 8 * 2 * 32);
   const Group g(a.tpr);
-  float(*slot)[32] = red[g.bar - 1];
-  int flip = 0;
-  using V = RowVec<T, VW>;
+  using L = Lane<T, VW, NV>;
+  constexpr int NP = L::NP;
   const T *o = static_cast<const T *>(a.o), *h = static_cast<const T *>(a.h), *gate = static_cast<const T *>(a.gate);
   T *ho = static_cast<T *>(a.h_out), *n = static_cast<T *>(a.n);
   const int64_t r0 = g.id * a.rows_per_group;
   const int64_t r1 = r0 + a.rows_per_group < a.T ? r0 + a.rows_per_group : a.T;
   if (r0 >= r1) return;
-  float wq[NV][VW], wn[NV][VW];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (g.tid + j * a.tpr) * VW;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      wq[j][e] = a.beta * (a.w_post && c < a.d ? a.w_post[c + e] : 1.f);
-      wn[j][e] = a.w_pre && c < a.d ? a.w_pre[c + e] : 1.f;
-    }
+  constexpr bool EACH = GK == GK_EACH, SHARED = GK == GK_SHARED;
+  float *slot = red[g.bar - 1][0], *other = red[g.bar - 1][1];
+  L vo, vh, vg;
+  vo.clear();
+  vh.clear();
+  vg.clear();
+  Ring<S, NV> ring;
+  if (S) {
+    ring.init(1 + (o ? 1 : 0) + (EACH ? 1 : 0));
+    if (g.tid * VW >= a.d) ring.zero(S);
   }
-  V vo[NV], vh[NV], vg[NV];
-  auto load = [&](int64_t r) {
+  auto load = [&](int64_t r, int st) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-        if (o) vo[j].load(o + r * a.ldo + c);
-        vh[j].load(h + r * a.ldh + c);
+      if (c < a.d && r < r1) {
+        if constexpr (S > 0) {
+          ring.copy(ring.at(st, 0, j), h + r * a.ldh + c);
+          if (o) ring.copy(ring.at(st, 1, j), o + r * a.ldo + c);
+          if (EACH) ring.copy(ring.at(st, 2, j), gate + r * a.ldg + c);
+        } else {
+          vh.v[j].load(h + r * a.ldh + c);
+          if (o) vo.v[j].load(o + r * a.ldo + c);
+          if (EACH) vg.v[j].load(gate + r * a.ldg + c);
+        }
       }
     }
+    if constexpr (S > 0) ring.commit();
   };
-  load(r0);
-  int64_t grow = r0 / a.gate_rows, gnext = grow * a.gate_rows;  // the gate row in registers is loaded at gnext
+  int st = 0;
+  if constexpr (S > 0) {
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) load(r0 + k, k);
+  } else {
+    load(r0, 0);
+  }
+  // beta w_post, times a gate that rows share
+  float2 wq[NP], wn[NP];
+  gains<VW, NV>(wn, a.w_pre, g.tid, a.tpr, a.d);
+  auto branch_gains = [&]() {
+    gains<VW, NV>(wq, a.w_post, g.tid, a.tpr, a.d);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) wq[p] = mul2(wq[p], both(a.beta));
+  };
+  branch_gains();
+  int64_t grow = r0 / a.gate_rows, gnext = a.gate_kind != POET_GATE_NONE && !EACH ? r0 : a.T;
   float gval = 1.f;
   const float inv_d = 1.f / float(a.d);
+  const float2 alpha = both(a.alpha);
   for (int64_t r = r0; r < r1; ++r) {
-    if (a.gate_kind != POET_GATE_NONE && (r == r0 || r == gnext)) {
-      if (r == gnext && r != r0) ++grow;
+    if (r == gnext) {  // the next gate row
+      if (r != r0) ++grow;
       gnext = (grow + 1) * a.gate_rows;
-      if (a.gate_kind == POET_GATE_ROW) {
+      if (!SHARED) {
         gval = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
       } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int c = (g.tid + j * a.tpr) * VW;
-          if (c < a.d) vg[j].load(gate + grow * a.ldg + c);
+          if (c < a.d) vg.v[j].load(gate + grow * a.ldg + c);
         }
+        float2 gv[NP];
+        vg.get(gv);
+        branch_gains();
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          wq[p] = mul2(wq[p], make_float2(act_of(gv[p].x, a.gate_sigmoid), act_of(gv[p].y, a.gate_sigmoid)));
       }
     }
-    float x[NV][VW], q[NV][VW];
+    if constexpr (S > 0) {
+      ring.wait();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-        vh[j].get(x[j]);
-        if (o) vo[j].get(q[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) x[j][e] = q[j][e] = 0.f;
+      for (int j = 0; j < NV; ++j) {
+        ring.read(vh.v[j], ring.at(st, 0, j));
+        if (o) ring.read(vo.v[j], ring.at(st, 1, j));
+        if (EACH) ring.read(vg.v[j], ring.at(st, 2, j));
       }
     }
-    if (r + 1 < r1) load(r + 1);
+    float2 x[NP];
+    vh.get(x);
     if (o) {
+      float2 q[NP];
+      vo.get(q);
       float ro = gval;
       if (a.post) {
-        float s[1] = {0.f};
+        float2 s2 = both(0.f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < VW; ++e) s[0] = fmaf(q[j][e], q[j][e], s[0]);
-        row_sum<1>(s, slot[flip], g.warps, g.warp, g.bar, a.tpr);
-        flip ^= 1;
-        ro = gval / sqrtf(s[0] * inv_d + a.eps);
+        for (int p = 0; p < NP; ++p) s2 = fma2(q[p], q[p], s2);
+        float s[1] = {s2.x + s2.y};
+        row_sum<1>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+        float *const was = slot;
+        slot = other;
+        other = was;
+        ro *= inv_sqrt(fmaf(s[0], inv_d, a.eps));
       }
+      if (EACH) {
+        float2 gv[NP];
+        vg.get(gv);
+        if (a.gate_sigmoid) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (g.tid + j * a.tpr) * VW;
-        float gv[VW];
-        if (a.gate_kind == POET_GATE_CHANNEL && c < a.d) {
-          vg[j].get(gv);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) gv[e] = act_of(gv[e], a.gate_sigmoid);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) gv[e] = 1.f;
+          for (int p = 0; p < NP; ++p) gv[p] = make_float2(sigmoid(gv[p].x), sigmoid(gv[p].y));
         }
 #pragma unroll
-        for (int e = 0; e < VW; ++e) x[j][e] = fmaf(a.alpha, x[j][e], q[j][e] * ro * wq[j][e] * gv[e]);
-        if (c < a.d) V::store(ho + r * a.ldho + c, x[j]);
+        for (int p = 0; p < NP; ++p) q[p] = mul2(q[p], gv[p]);
       }
+#pragma unroll
+      for (int p = 0; p < NP; ++p) x[p] = fma2(mul2(q[p], both(ro)), wq[p], mul2(x[p], alpha));
+      L::put(ho + r * a.ldho, g.tid, a.tpr, a.d, x);
+    }
+    if constexpr (S > 0) {
+      load(r + S - 1, st == 0 ? S - 1 : st - 1);
+      st = st + 1 == S ? 0 : st + 1;
+    } else {
+      load(r + 1, 0);
     }
     if (n) {
-      float s[1] = {0.f};
+      float2 s2 = both(0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int p = 0; p < NP; ++p) s2 = fma2(x[p], x[p], s2);
+      float s[1] = {s2.x + s2.y};
+      row_sum<1>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+      float *const was = slot;
+      slot = other;
+      other = was;
+      const float2 rn = both(inv_sqrt(fmaf(s[0], inv_d, a.eps)));
 #pragma unroll
-        for (int e = 0; e < VW; ++e) s[0] = fmaf(x[j][e], x[j][e], s[0]);
-      row_sum<1>(s, slot[flip], g.warps, g.warp, g.bar, a.tpr);
-      flip ^= 1;
-      const float rn = 1.f / sqrtf(s[0] * inv_d + a.eps);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (g.tid + j * a.tpr) * VW;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) x[j][e] *= rn * wn[j][e];
-        if (c < a.d) V::store(n + r * a.ldn + c, x[j]);
-      }
+      for (int p = 0; p < NP; ++p) x[p] = mul2(mul2(x[p], rn), wn[p]);
+      L::put(n + r * a.ldn, g.tid, a.tpr, a.d, x);
     }
   }
 }
@@ -182,12 +349,13 @@ struct JointBwdArgs {
   float alpha, beta, eps;
 };
 
-template <typename T, int VW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) joint_bwd_kernel(const JointBwdArgs a) {
-  __shared__ float red[8][2][3][32];
+template <typename T, int VW, int NV, int S, int GK, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArgs a) {
+  __shared__ __align__(16) float red[8][2][4 * 32];
+  zero_slots(red[0][0], 8 * 2 * 4 * 32);
   const Group g(a.tpr);
-  float(*slot)[3][32] = red[g.bar - 1];
-  using V = RowVec<T, VW>;
+  using L = Lane<T, VW, NV>;
+  constexpr int NP = L::NP;
   const T *o = static_cast<const T *>(a.o), *hp = static_cast<const T *>(a.hp), *gate = static_cast<const T *>(a.gate);
   const T *dhp = static_cast<const T *>(a.dhp), *dn = static_cast<const T *>(a.dn);
   T *dh = static_cast<T *>(a.dh), *d_o = static_cast<T *>(a.d_o), *dgate = static_cast<T *>(a.dgate);
@@ -203,49 +371,72 @@ __global__ void __launch_bounds__(MAXT) joint_bwd_kernel(const JointBwdArgs a) {
     r1 = r0 + a.segs_per_group * a.seg_rows < a.T ? r0 + a.segs_per_group * a.seg_rows : a.T;
     if (r0 >= a.T) return;
   }
+  constexpr bool EACH = GK == GK_EACH, SHARED = GK == GK_SHARED;
   const bool shared_gate = dgate && a.gate_rows > 1;
-  float aq[NV][VW], an[NV][VW], ag[NV][VW];
+  float *slot = red[g.bar - 1][0], *other = red[g.bar - 1][1];
+  float2 aq[NP], an[NP], ag[NP];  // column sums
   float ag_row = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < VW; ++e) aq[j][e] = an[j][e] = ag[j][e] = 0.f;
+  for (int p = 0; p < NP; ++p) aq[p] = an[p] = ag[p] = both(0.f);
   const float inv_d = 1.f / float(a.d);
-  V vo[NV], vh[NV], vd[NV], vn[NV], vg[NV];
-  auto load = [&](int64_t r) {
+  const float2 alpha = both(o ? a.alpha : 1.f), beta = both(a.beta);
+  L vo, vh, vd, vn, vg;
+  vo.clear();
+  vh.clear();
+  vd.clear();
+  vn.clear();
+  vg.clear();
+  const int sd = dn ? 2 : 0, so = sd + (dhp ? 1 : 0), sg = so + (o ? 1 : 0);  // places in the ring: h', dn first
+  Ring<S, NV> ring;
+  constexpr bool GR = EACH && S > 2;  // a gate of the row's own in the ring; with two stages there is no room for it
+  if (S) {
+    ring.init(sg + (GR ? 1 : 0));
+    if (g.tid * VW >= a.d) ring.zero(S);
+  }
+  auto load = [&](int64_t r, int st) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-        if (o) vo[j].load(o + r * a.ldo + c);
-        if (dn) {
-          vh[j].load(hp + r * a.ldhp + c);
-          vn[j].load(dn + r * a.lddn + c);
+      if (c < a.d && r < r1) {
+        if constexpr (S > 0) {
+          if (dn) {
+            ring.copy(ring.at(st, 0, j), hp + r * a.ldhp + c);
+            ring.copy(ring.at(st, 1, j), dn + r * a.lddn + c);
+          }
+          if (dhp) ring.copy(ring.at(st, sd, j), dhp + r * a.lddhp + c);
+          if (o) ring.copy(ring.at(st, so, j), o + r * a.ldo + c);
+          if (GR) ring.copy(ring.at(st, sg, j), gate + r * a.ldg + c);
+        } else {
+          if (dn) {
+            vh.v[j].load(hp + r * a.ldhp + c);
+            vn.v[j].load(dn + r * a.lddn + c);
+          }
+          if (dhp) vd.v[j].load(dhp + r * a.lddhp + c);
+          if (o) vo.v[j].load(o + r * a.ldo + c);
+          if (EACH) vg.v[j].load(gate + r * a.ldg + c);
         }
-        if (dhp) vd[j].load(dhp + r * a.lddhp + c);
       }
     }
+    if constexpr (S > 0) ring.commit();
   };
-  if (r0 < r1) load(r0);
-  int64_t grow = r0 / a.gate_rows, gnext = (grow + 1) * a.gate_rows;
-  float graw = 0.f;
-  auto load_gate = [&]() {
-    if (a.gate_kind == POET_GATE_ROW) {
-      graw = to_float(gate[grow * a.ldg]);
-    } else if (a.gate_kind == POET_GATE_CHANNEL) {
+  int st = 0;
+  if constexpr (S > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (g.tid + j * a.tpr) * VW;
-        if (c < a.d) vg[j].load(gate + grow * a.ldg + c);
-      }
-    }
-  };
+    for (int k = 0; k < S - 1; ++k) load(r0 + k, k);
+  } else {
+    load(r0, 0);
+  }
+  Gains<VW, NV, (S > 0)> gq, gn;
+  const uint32_t gains_at = ring.base - threadIdx.x * 16 + S * ring.stage;
+  gq.init(a.w_post, gains_at, g.tid, a.tpr, a.d);
+  gn.init(a.w_pre, gains_at + blockDim.x * VW * NV * 4, g.tid, a.tpr, a.d);
   // The gradient of the gate row in registers: to the result, or (where several
   // groups share the row) to this group's partial sums.
+  int64_t grow = r0 / a.gate_rows;
   auto flush_gate = [&]() {
-    if (!shared_gate) return;
+    if (EACH || !shared_gate) return;
     const bool part = a.chunks > 1;
-    if (a.gate_kind == POET_GATE_ROW) {
+    if (!SHARED) {
       if (g.tid == 0) {
         if (part) a.part_gate[g.id] = ag_row;
         else dgate[grow * a.lddg] = from_float<T>(ag_row);
@@ -253,140 +444,170 @@ __global__ void __launch_bounds__(MAXT) joint_bwd_kernel(const JointBwdArgs a) {
       ag_row = 0.f;
       return;
     }
+    if (part) put_floats<VW, NV>(a.part_gate + g.id * a.d, g.tid, a.tpr, a.d, ag);
+    else L::put(dgate + grow * a.lddg, g.tid, a.tpr, a.d, ag);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) a.part_gate[g.id * a.d + c + e] = ag[j][e];
-        } else {
-          V::store(dgate + grow * a.lddg + c, ag[j]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) ag[j][e] = 0.f;
-    }
+    for (int p = 0; p < NP; ++p) ag[p] = both(0.f);
   };
-  if (r0 < r1) load_gate();
+  float ga_row = 1.f, sl_row = 1.f;  // a row gate's value and slope
+  int64_t gnext = a.gate_kind != POET_GATE_NONE && !EACH ? r0 : a.T;
   for (int64_t r = r0; r < r1; ++r) {
-    if (r == gnext && a.gate_kind != POET_GATE_NONE) {
-      flush_gate();
-      ++grow;
-      gnext += a.gate_rows;
-      load_gate();
-    }
-    // x: h', then t; y: dn; q: o
-    float x[NV][VW], y[NV][VW], q[NV][VW], t[NV][VW];
-    float s[3] = {0.f, 0.f, 0.f};  // sum h'^2, sum u h', sum o^2
+    if (r == gnext) {  // the next gate row
+      if (r != r0) {
+        flush_gate();
+        ++grow;
+      }
+      gnext = (grow + 1) * a.gate_rows;
+      if (!SHARED) {
+        ga_row = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
+        sl_row = a.gate_sigmoid ? ga_row * (1.f - ga_row) : 1.f;
+      } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-#pragma unroll
-      for (int e = 0; e < VW; ++e) x[j][e] = y[j][e] = q[j][e] = t[j][e] = 0.f;
-      if (c < a.d) {
-        if (dn) {
-          vh[j].get(x[j]);
-          vn[j].get(y[j]);
-        }
-        if (dhp) vd[j].get(t[j]);
-        if (o) vo[j].get(q[j]);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          s[0] = fmaf(x[j][e], x[j][e], s[0]);
-          s[1] = fmaf(a.w_pre ? y[j][e] * a.w_pre[c + e] : y[j][e], x[j][e], s[1]);
-          s[2] = fmaf(q[j][e], q[j][e], s[2]);
+        for (int j = 0; j < NV; ++j) {
+          const int c = (g.tid + j * a.tpr) * VW;
+          if (c < a.d) vg.v[j].load(gate + grow * a.ldg + c);
         }
       }
     }
-    if (r + 1 < r1) load(r + 1);
-    row_sum<3>(s, slot[0][0], g.warps, g.warp, g.bar, a.tpr);
-    const float rn = 1.f / sqrtf(s[0] * inv_d + a.eps);
-    const float mn = s[1] * rn * inv_d;  // mean(u nh)
-    const float ro = a.post ? 1.f / sqrtf(s[2] * inv_d + a.eps) : 1.f;
-    const float grv = a.gate_kind == POET_GATE_ROW ? act_of(graw, a.gate_sigmoid) : 1.f;
-    float w[2] = {0.f, 0.f};  // sum v ph, sum of the row gate's gradient
+    // First pass over the row: its sums.  The second pass takes the operands from
+    // the ring again rather than hold them in registers across the exchange.
+    auto fetch = [&](L &v, int place) {
+      if constexpr (S > 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-        float gv[VW];
-        if (a.gate_kind == POET_GATE_CHANNEL) vg[j].get(gv);
-        float dg[VW], out[VW];
+        for (int j = 0; j < NV; ++j) ring.read(v.v[j], ring.at(st, place, j));
+      }
+    };
+    if constexpr (S > 0) ring.wait();
+    if (EACH && S > 0 && !GR) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          if (dn) {
-            const float nh = x[j][e] * rn;
-            an[j][e] = fmaf(y[j][e], nh, an[j][e]);
-            const float u = a.w_pre ? y[j][e] * a.w_pre[c + e] : y[j][e];
-            t[j][e] = fmaf(u - nh * mn, rn, t[j][e]);
-          }
-          out[e] = o ? a.alpha * t[j][e] : t[j][e];
-        }
-        V::store(dh + r * a.lddh + c, out);
-        if (o) {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float ga = a.gate_kind == POET_GATE_CHANNEL ? act_of(gv[e], a.gate_sigmoid) : grv;
-            const float da = a.beta * t[j][e];
-            const float dp = da * ga;
-            const float ph = q[j][e] * ro;
-            const float wp = a.w_post ? a.w_post[c + e] : 1.f;
-            dg[e] = da * (ph * wp) * (a.gate_sigmoid ? ga * (1.f - ga) : 1.f);
-            if (a.post) aq[j][e] = fmaf(dp, ph, aq[j][e]);
-            const float v = dp * wp;
-            w[0] = fmaf(v, ph, w[0]);
-            w[1] += dg[e];
-            t[j][e] = v;
-            q[j][e] = ph;
-          }
-          if (dgate && a.gate_kind == POET_GATE_CHANNEL) {
-            if (a.gate_rows == 1) {
-              V::store(dgate + r * a.lddg + c, dg);
-            } else {
-#pragma unroll
-              for (int e = 0; e < VW; ++e) ag[j][e] += dg[e];
-            }
-          }
-        }
+      for (int j = 0; j < NV; ++j) {
+        const int c = (g.tid + j * a.tpr) * VW;
+        if (c < a.d) vg.v[j].load(gate + r * a.ldg + c);
       }
     }
-    if (!o) {
-      // the buffer of the first sum is written again in the next row: keep the two-barrier order
-      if (g.warps > 1) asm volatile("bar.sync %0, %1;" ::"r"(g.bar), "r"(a.tpr) : "memory");
+    float s[4] = {0.f, 0.f, 0.f, 0.f};  // sum h'^2, sum u h', sum o^2
+    if (dn) {
+      float2 x[NP], y[NP], wn[NP], s0 = both(0.f), s1 = both(0.f);
+      fetch(vh, 0);
+      fetch(vn, 1);
+      vh.get(x);
+      vn.get(y);
+      gn.get(wn);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        s0 = fma2(x[p], x[p], s0);
+        s1 = fma2(mul2(y[p], wn[p]), x[p], s1);
+      }
+      s[0] = s0.x + s0.y;
+      s[1] = s1.x + s1.y;
+    }
+    if (o && a.post) {
+      float2 x[NP], s2 = both(0.f);
+      fetch(vo, so);
+      vo.get(x);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) s2 = fma2(x[p], x[p], s2);
+      s[2] = s2.x + s2.y;
+    }
+    row_sum<4>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+    const float rn = inv_sqrt(fmaf(s[0], inv_d, a.eps)), mn = s[1] * rn * inv_d;  // 1 / r', mean(u nh)
+    const float ro = a.post ? inv_sqrt(fmaf(s[2], inv_d, a.eps)) : 1.f;           // 1 / r
+    float2 t[NP], q[NP];  // t, then v; ph
+    if (dhp) {
+      fetch(vd, sd);
+      vd.get(t);
+    } else {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) t[p] = both(0.f);
+    }
+    if (dn) {
+      float2 x[NP], y[NP], wn[NP];
+      fetch(vh, 0);
+      fetch(vn, 1);
+      vh.get(x);
+      vn.get(y);
+      gn.get(wn);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const float2 nh = mul2(x[p], both(rn));
+        an[p] = fma2(y[p], nh, an[p]);
+        t[p] = fma2(mul2(y[p], wn[p]), both(rn), t[p]);
+        t[p] = fma2(nh, both(-mn * rn), t[p]);
+      }
+    }
+    {
+      float2 out[NP];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) out[p] = mul2(t[p], alpha);
+      L::put(dh + r * a.lddh, g.tid, a.tpr, a.d, out);
+    }
+    float w[2] = {0.f, 0.f};  // sum v ph, sum of the row gate's gradient before its slope
+    if (o) {
+      float2 w0 = both(0.f), w1 = both(0.f), dg[NP], wq[NP];
+      fetch(vo, so);
+      if (GR) fetch(vg, sg);
+      vo.get(q);
+      if (EACH || SHARED) vg.get(dg);
+      gq.get(wq);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        float2 ga = both(ga_row);
+        if (EACH || SHARED) {
+          ga = dg[p];
+          if (a.gate_sigmoid) ga = make_float2(sigmoid(ga.x), sigmoid(ga.y));
+        }
+        const float2 da = mul2(t[p], beta), dp = mul2(da, ga);
+        q[p] = mul2(q[p], both(ro));
+        const float2 z = mul2(q[p], wq[p]);
+        aq[p] = fma2(dp, q[p], aq[p]);
+        t[p] = mul2(dp, wq[p]);
+        w0 = fma2(dp, z, w0);
+        if (EACH || SHARED) {
+          dg[p] = mul2(da, z);
+          if (a.gate_sigmoid) dg[p] = mul2(dg[p], fma2(ga, mul2(ga, both(-1.f)), ga));
+          if (SHARED) ag[p] = add2(ag[p], dg[p]);
+        } else {
+          w1 = fma2(da, z, w1);
+        }
+      }
+      if (EACH && dgate) L::put(dgate + r * a.lddg, g.tid, a.tpr, a.d, dg);
+      w[0] = w0.x + w0.y;
+      w[1] = w1.x + w1.y;
+    }
+    if constexpr (S > 0) {
+      load(r + S - 1, st == 0 ? S - 1 : st - 1);
+      st = st + 1 == S ? 0 : st + 1;
+    } else {
+      load(r + 1, 0);
+    }
+    if (!o) {  // one sum a row: its buffers alternate
+      float *const was = slot;
+      slot = other;
+      other = was;
       continue;
     }
-    row_sum<2>(w, slot[1][0], g.warps, g.warp, g.bar, a.tpr);
-    const float mo = a.post ? w[0] * inv_d : 0.f;  // mean(v ph)
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d) {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) t[j][e] = (t[j][e] - q[j][e] * mo) * ro;
-        V::store(d_o + r * a.lddo + c, t[j]);
-      }
+    if (a.post || (dgate && a.gate_kind == POET_GATE_ROW)) {
+      row_sum<2>(w, other, g.warps, g.warp, g.bar, a.tpr);
+    } else if (g.warps > 1) {  // the first sum's buffer is written again in the next row
+      asm volatile("bar.sync %0, %1;" ::"r"(g.bar), "r"(a.tpr) : "memory");
     }
-    if (dgate && a.gate_kind == POET_GATE_ROW) {
+    if (a.post) {
+      const float2 mo = both(-w[0] * inv_d);  // -mean(v ph)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) t[p] = mul2(fma2(q[p], mo, t[p]), both(ro));
+    }
+    L::put(d_o + r * a.lddo, g.tid, a.tpr, a.d, t);
+    if (!EACH && !SHARED && dgate) {
       if (a.gate_rows == 1) {
-        if (g.tid == 0) dgate[r * a.lddg] = from_float<T>(w[1]);
+        if (g.tid == 0) dgate[r * a.lddg] = from_float<T>(w[1] * sl_row);
       } else {
-        ag_row += w[1];
+        ag_row += w[1] * sl_row;
       }
     }
   }
   flush_gate();
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (g.tid + j * a.tpr) * VW;
-    if (c < a.d) {
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        if (a.part_post) a.part_post[g.id * a.d + c + e] = aq[j][e];
-        if (a.part_pre) a.part_pre[g.id * a.d + c + e] = an[j][e];
-      }
-    }
-  }
+  if (a.part_post) put_floats<VW, NV>(a.part_post + g.id * a.d, g.tid, a.tpr, a.d, aq);
+  if (a.part_pre) put_floats<VW, NV>(a.part_pre + g.id * a.d, g.tid, a.tpr, a.d, an);
 }
 
 // Column sums of the groups' partial sums, in the groups' order.  Block (x, y):
@@ -475,10 +696,14 @@ BwdPlan bwd_plan(const poet_joint *J, int64_t T, int64_t most) {
   return p;
 }
 
-// Most groups of rows: enough threads to fill every SM once more than over, and at
-// least four rows each (a group's partial sums cost as much as a row).
-int64_t bwd_most(int64_t T, int tpr) {
-  const int64_t fill = std::max<int64_t>(1, int64_t(num_sms()) * std::max(1, 1536 / tpr));
+// CTAs that an SM holds (what the kernels' launch bounds ask for).
+int fwd_resident(int threads) { return threads <= 256 ? 3 : 1; }
+int bwd_resident(int threads) { return threads <= 320 ? 2 : 1; }
+
+// Most groups of rows in the backward: what runs at once, and at least four rows
+// each (a group's partial sums cost as much as a row).
+int64_t bwd_most(int64_t T, const RowShape &s) {
+  const int64_t fill = int64_t(num_sms()) * bwd_resident(s.threads) * s.groups_per_cta;
   return std::max<int64_t>(1, std::min(fill, (T + 3) / 4));
 }
 
@@ -512,24 +737,78 @@ poet_status check_rows(const char *what, const char *name, const void *p, int64_
 // Whether every row of p starts on 16 bytes.
 bool rows16(const void *p, int64_t ld, int dtype) { return !p || (al16(p) && ld * int64_t(esize(dtype)) % 16 == 0); }
 
-template <typename T, int VW, int NV>
-poet_status launch_fwd(const JointFwdArgs &a, const RowShape &s, int64_t groups, cudaStream_t st) {
+template <auto KERN, typename A>
+poet_status launch_joint(const A &a, const RowShape &s, int64_t groups, size_t smem, cudaStream_t st, const char *what) {
   const unsigned grid = unsigned((groups + s.groups_per_cta - 1) / s.groups_per_cta);
-  if (s.threads <= 256) joint_fwd_kernel<T, VW, NV, 256><<<grid, s.threads, 0, st>>>(a);
-  else if (s.threads <= 512) joint_fwd_kernel<T, VW, NV, 512><<<grid, s.threads, 0, st>>>(a);
-  else joint_fwd_kernel<T, VW, NV, 1024><<<grid, s.threads, 0, st>>>(a);
+  POET_TRY(allow_smem<KERN>(smem));
+  KERN<<<grid, s.threads, smem, st>>>(a);
   count_launch();
-  return launch_status("joint");
+  return launch_status(what);
 }
 
-template <typename T, int VW, int NV>
-poet_status launch_bwd(const JointBwdArgs &a, const RowShape &s, int64_t groups, cudaStream_t st) {
-  const unsigned grid = unsigned((groups + s.groups_per_cta - 1) / s.groups_per_cta);
-  if (s.threads <= 256) joint_bwd_kernel<T, VW, NV, 256><<<grid, s.threads, 0, st>>>(a);
-  else if (s.threads <= 512) joint_bwd_kernel<T, VW, NV, 512><<<grid, s.threads, 0, st>>>(a);
-  else joint_bwd_kernel<T, VW, NV, 1024><<<grid, s.threads, 0, st>>>(a);
-  count_launch();
-  return launch_status("joint_bwd");
+// Rows of one 16-byte vector per thread go through the ring: four stages up to
+// 512 threads, two up to 1024 (four would not fit).  Wider rows, and rows that
+// do not start on 16 bytes, are read directly.
+template <typename T, int VW, int GK>
+poet_status launch_fwd(const JointFwdArgs &a, const RowShape &s, int64_t groups, int operands, cudaStream_t st) {
+  const size_t stage = size_t(s.threads) * 16 * operands;
+  if (s.nv == 1) {
+    if (s.threads <= 256) return launch_joint<joint_fwd_kernel<T, VW, 1, 4, GK, 256, 3>>(a, s, groups, 4 * stage, st, "joint");
+    if (s.threads <= 512) return launch_joint<joint_fwd_kernel<T, VW, 1, 4, GK, 512, 1>>(a, s, groups, 4 * stage, st, "joint");
+    return launch_joint<joint_fwd_kernel<T, VW, 1, 2, GK, 1024, 1>>(a, s, groups, 2 * stage, st, "joint");
+  }
+  if (s.nv == 2) return launch_joint<joint_fwd_kernel<T, VW, 2, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
+  return launch_joint<joint_fwd_kernel<T, VW, 4, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
+}
+template <typename T, int GK>
+poet_status launch_fwd_scalar(const JointFwdArgs &a, const RowShape &s, int64_t groups, cudaStream_t st) {
+  if (s.nv == 8) {
+    if (s.threads <= 256) return launch_joint<joint_fwd_kernel<T, 1, 8, 0, GK, 256, 3>>(a, s, groups, 0, st, "joint");
+    return launch_joint<joint_fwd_kernel<T, 1, 8, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
+  }
+  return launch_joint<joint_fwd_kernel<T, 1, 16, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
+}
+
+template <typename T, int VW, int GK>
+poet_status launch_bwd(const JointBwdArgs &a, const RowShape &s, int64_t groups, int operands, cudaStream_t st) {
+  const size_t stage = size_t(s.threads) * 16, gains = size_t(s.threads) * VW * 8;
+  const int each = GK == GK_EACH ? 1 : 0;  // with two stages the gate is not in the ring
+  const size_t four = 4 * stage * (operands + each) + gains, two = 2 * stage * operands + gains;
+  if (s.nv == 1) {
+    if (s.threads <= 256)
+      return launch_joint<joint_bwd_kernel<T, VW, 1, 4, GK, 256, 2>>(a, s, groups, four, st, "joint_bwd");
+    if (s.threads <= 320)
+      return launch_joint<joint_bwd_kernel<T, VW, 1, 3, GK, 320, 2>>(a, s, groups, four - stage * (operands + each), st,
+                          "joint_bwd");
+    if (s.threads <= 512)
+      return launch_joint<joint_bwd_kernel<T, VW, 1, 4, GK, 512, 1>>(a, s, groups, four, st, "joint_bwd");
+    return launch_joint<joint_bwd_kernel<T, VW, 1, 2, GK, 1024, 1>>(a, s, groups, two, st, "joint_bwd");
+  }
+  if (s.nv == 2) return launch_joint<joint_bwd_kernel<T, VW, 2, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint_bwd");
+  return launch_joint<joint_bwd_kernel<T, VW, 4, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint_bwd");
+}
+template <typename T, int GK>
+poet_status launch_bwd_scalar(const JointBwdArgs &a, const RowShape &s, int64_t groups, cudaStream_t st) {
+  if (s.nv == 8) {
+    if (s.threads <= 256) return launch_joint<joint_bwd_kernel<T, 1, 8, 0, GK, 256, 2>>(a, s, groups, 0, st, "joint_bwd");
+    return launch_joint<joint_bwd_kernel<T, 1, 8, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint_bwd");
+  }
+  return launch_joint<joint_bwd_kernel<T, 1, 16, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint_bwd");
+}
+
+template <int GK>
+poet_status pick_fwd(const JointFwdArgs &a, const RowShape &s, int64_t groups, int operands, int dt, bool vec,
+                     cudaStream_t st) {
+  if (dt == POET_BF16)
+    return vec ? launch_fwd<bf16, 8, GK>(a, s, groups, operands, st) : launch_fwd_scalar<bf16, GK>(a, s, groups, st);
+  return vec ? launch_fwd<float, 4, GK>(a, s, groups, operands, st) : launch_fwd_scalar<float, GK>(a, s, groups, st);
+}
+template <int GK>
+poet_status pick_bwd(const JointBwdArgs &a, const RowShape &s, int64_t groups, int operands, int dt, bool vec,
+                     cudaStream_t st) {
+  if (dt == POET_BF16)
+    return vec ? launch_bwd<bf16, 8, GK>(a, s, groups, operands, st) : launch_bwd_scalar<bf16, GK>(a, s, groups, st);
+  return vec ? launch_bwd<float, 4, GK>(a, s, groups, operands, st) : launch_bwd_scalar<float, GK>(a, s, groups, st);
 }
 
 }  // namespace
@@ -575,7 +854,7 @@ poet_status poet_joint_forward(const poet_joint *J, const void *o, int64_t ldo, 
                    rows16(n, ldn, dt) && (a.gate_kind != POET_GATE_CHANNEL || rows16(gate, ldg, dt));
   const RowShape s = row_shape(d, vec ? vw : 1, vec ? 1 : 8);
   a.tpr = s.tpr;
-  const int64_t fill = std::max<int64_t>(1, int64_t(num_sms()) * (2048 / s.tpr));
+  const int64_t fill = int64_t(num_sms()) * fwd_resident(s.threads) * s.groups_per_cta;
   a.rows_per_group = (T + fill - 1) / fill;
   const int64_t groups = (T + a.rows_per_group - 1) / a.rows_per_group;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -583,15 +862,11 @@ poet_status poet_joint_forward(const poet_joint *J, const void *o, int64_t ldo, 
   const double gate_elems = a.gate_kind == POET_GATE_CHANNEL ? double(G) * d : a.gate_kind == POET_GATE_ROW ? double(G) : 0.0;
   TraceScope ts("joint", 14.0 * double(T) * d,
                 (double(T) * d * ((o ? 3 : 1) + (n ? 1 : 0)) + gate_elems) * double(esize(dt)), st);
-  if (dt == POET_BF16) {
-    if (vec) return s.nv == 1 ? launch_fwd<bf16, 8, 1>(a, s, groups, st) : launch_fwd<bf16, 8, 2>(a, s, groups, st);
-    return s.nv == 8 ? launch_fwd<bf16, 1, 8>(a, s, groups, st) : launch_fwd<bf16, 1, 16>(a, s, groups, st);
-  }
-  if (vec) {
-    if (s.nv == 1) return launch_fwd<float, 4, 1>(a, s, groups, st);
-    return s.nv == 2 ? launch_fwd<float, 4, 2>(a, s, groups, st) : launch_fwd<float, 4, 4>(a, s, groups, st);
-  }
-  return s.nv == 8 ? launch_fwd<float, 1, 8>(a, s, groups, st) : launch_fwd<float, 1, 16>(a, s, groups, st);
+  const bool channel = a.gate_kind == POET_GATE_CHANNEL;
+  const int operands = 1 + (o ? 1 : 0) + (channel && J->gate_rows == 1 ? 1 : 0);
+  if (!channel) return pick_fwd<GK_ROW>(a, s, groups, operands, dt, vec, st);
+  return J->gate_rows == 1 ? pick_fwd<GK_EACH>(a, s, groups, operands, dt, vec, st)
+                           : pick_fwd<GK_SHARED>(a, s, groups, operands, dt, vec, st);
 }
 
 size_t poet_joint_workspace_bytes(const poet_joint *J, int64_t T) {
@@ -604,7 +879,7 @@ size_t poet_joint_workspace_bytes(const poet_joint *J, int64_t T) {
   size_t most = 0;
   for (int k = 0; k < 2; ++k) {
     const RowShape s = row_shape(J->d, k == 0 ? vw : 1, k == 0 ? 1 : 8);
-    most = std::max(most, size_t(bwd_most(T, s.tpr)));
+    most = std::max(most, size_t(bwd_most(T, s)));
   }
   return 3 * align256(most * size_t(J->d) * 4);
 }
@@ -672,7 +947,7 @@ poet_status poet_joint_backward(const poet_joint *J, const void *o, int64_t ldo,
                    (!channel || (rows16(gate, ldg, dt) && rows16(dgate, lddg, dt)));
   const RowShape s = row_shape(d, vec ? vw : 1, vec ? 1 : 8);
   a.tpr = s.tpr;
-  const BwdPlan p = bwd_plan(J, T, bwd_most(T, s.tpr));
+  const BwdPlan p = bwd_plan(J, T, bwd_most(T, s));
   a.seg_rows = p.seg_rows; a.chunks = p.chunks; a.segs_per_group = p.segs_per_group;
   const size_t part = align256(size_t(p.groups) * d * 4);
   char *wb = static_cast<char *>(ws);
@@ -683,18 +958,10 @@ poet_status poet_joint_backward(const poet_joint *J, const void *o, int64_t ldo,
   const double gate_elems = channel ? 2.0 * double(G) * d : a.gate_kind == POET_GATE_ROW ? 2.0 * double(G) : 0.0;
   const int passes = 1 + (o ? 2 : 0) + (dn ? 2 : 0) + (dh_out ? 1 : 0);
   TraceScope ts("joint_bwd", 30.0 * double(T) * d, (double(T) * d * passes + gate_elems) * double(esize(dt)), st);
-  poet_status rc;
-  if (dt == POET_BF16) {
-    if (vec) rc = s.nv == 1 ? launch_bwd<bf16, 8, 1>(a, s, p.groups, st) : launch_bwd<bf16, 8, 2>(a, s, p.groups, st);
-    else rc = s.nv == 8 ? launch_bwd<bf16, 1, 8>(a, s, p.groups, st) : launch_bwd<bf16, 1, 16>(a, s, p.groups, st);
-  } else if (vec) {
-    rc = s.nv == 1   ? launch_bwd<float, 4, 1>(a, s, p.groups, st)
-         : s.nv == 2 ? launch_bwd<float, 4, 2>(a, s, p.groups, st)
-                     : launch_bwd<float, 4, 4>(a, s, p.groups, st);
-  } else {
-    rc = s.nv == 8 ? launch_bwd<float, 1, 8>(a, s, p.groups, st) : launch_bwd<float, 1, 16>(a, s, p.groups, st);
-  }
-  POET_TRY(rc);
+  const int operands = (dn ? 2 : 0) + (dh_out ? 1 : 0) + (o ? 1 : 0);
+  if (!channel) POET_TRY(pick_bwd<GK_ROW>(a, s, p.groups, operands, dt, vec, st));
+  else if (J->gate_rows == 1) POET_TRY(pick_bwd<GK_EACH>(a, s, p.groups, operands, dt, vec, st));
+  else POET_TRY(pick_bwd<GK_SHARED>(a, s, p.groups, operands, dt, vec, st));
   const bool sum_gate = dgate && J->gate_rows > 1 && p.chunks > 1;
   if (!dw_post && !dw_pre && !sum_gate) return POET_OK;
   JointSumArgs u{};

@@ -890,7 +890,7 @@ bool al(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n -
 
 template <typename K, typename A>
 poet_status launch_rows(K kern, const A &a, int64_t T, int cluster, size_t smem, cudaStream_t st, const char *what) {
-  if (smem > 48 * 1024) POET_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  if (smem > 32 * 1024) POET_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -3,9 +3,31 @@
 // sums over the threads that share a row.
 #pragma once
 
+#include <atomic>
+
 #include "poet_internal.cuh"
 
 namespace poet {
+
+// Lets a kernel use all the dynamic shared memory that its static part leaves
+// of a block's on the current device, where a launch asks for `bytes` of it.
+// Asked of the runtime once per kernel and device.
+template <auto KERN>
+poet_status allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  if (bytes <= 32 * 1024) return POET_OK;  // with the static part below the default of 48 KB
+  int dev = 0;
+  POET_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return POET_OK;
+  int most = 0;
+  cudaFuncAttributes f;
+  POET_CUDA_TRY(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
+  POET_CUDA_TRY(cudaFuncGetAttributes(&f, KERN));
+  POET_CUDA_TRY(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, most - int(f.sharedSizeBytes)));
+  done.fetch_or(bit, std::memory_order_release);
+  return POET_OK;
+}
 
 // VW consecutive elements of a row: 16 bytes where rows are aligned, one
 // element where they are not.
@@ -71,27 +93,67 @@ __device__ __forceinline__ bf16 from_float<bf16>(float v) { return __float2bfloa
 template <>
 __device__ __forceinline__ float from_float<float>(float v) { return v; }
 
-// Sums v[0..N) over the `warps` warps that share a row; every thread gets the
-// totals, added in one fixed order.  One barrier: `slot` alternates between
-// two buffers, and a buffer is written again only after the barrier of the
-// other one, which no thread passes before all have read the first.
+// Two floats at a time: one instruction for both.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// 1 / sqrt(x) for x > 0: CUDA's approximation and one Newton step (0 for x = inf).
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float y = rsqrtf(x);
+  return y > 0.f ? fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y) : y;
+}
+
+// Sums v[0..N), N = 1, 2 or 4, over the `warps` warps that share a row; every
+// thread gets the totals, added in one fixed order.  Within a warp several
+// values are summed by one butterfly: its first steps exchange halves of the
+// values, so that N values take 4 + N (N = 1: 5) shuffles.  One barrier:
+// `slot` (N * 32 floats, 16-byte aligned, zero behind the last warp) alternates
+// between two buffers, and a buffer is written again only after the barrier of
+// the other one, which no thread passes before all have read the first.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float *slot, int warps, int warp, int bar, int threads) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
   const int lane = threadIdx.x & 31;
-  if (lane == 0)
+  float t;
+  if constexpr (N == 4) {
+    const bool hi = lane & 16, up = lane & 8;
+    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    t = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
+  } else if constexpr (N == 2) {
+    const bool hi = lane & 16;
+    t = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+  } else {
+    t = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+  }
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[i * 32 + warp] = v[i];
+  for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  constexpr int LANES = 32 / N;  // lanes that hold one value's total
+  if (warps == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = N == 1 ? t : __shfl_sync(0xffffffffu, t, i * LANES);
+    return;
+  }
+  if (lane % LANES == 0) slot[warp * N + lane / LANES] = t;
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = lane < warps ? slot[i * 32 + lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  const float4 *s4 = reinterpret_cast<const float4 *>(slot);
+  float2 lo = both(0.f), hi = both(0.f);
+  const int quads = (warps * N + 3) / 4;
+#pragma unroll 2
+  for (int i = 0; i < quads; ++i) {
+    const float4 f = s4[i];
+    lo = add2(lo, make_float2(f.x, f.y));
+    hi = add2(hi, make_float2(f.z, f.w));
+  }
+  if constexpr (N == 4) {
+    v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
+  } else if constexpr (N == 2) {
+    v[0] = lo.x + hi.x; v[1] = lo.y + hi.y;
+  } else {
+    v[0] = (lo.x + lo.y) + (hi.x + hi.y);
   }
 }
 

@@ -193,8 +193,9 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the address alone: building a Stream object costs as much as a launch
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def torch_dtype(dtype: int):
@@ -678,9 +679,11 @@ def _dtype_of(t, what):
 
 
 def _operand(t, name, shape, dtype, device, rows=True):
-    """A device operand: its address and row stride (rows contiguous), after checks."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    """A device operand: its address and row stride (rows contiguous), after checks.  device: its index."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -689,18 +692,34 @@ def _operand(t, name, shape, dtype, device, rows=True):
         if t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"the rows of {name} must be contiguous (stride(1) == 1)")
         return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr(), 1
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _current(t, name):
-    """The library launches on the current device: operands must be there."""
+    """The library launches on the current device: operands must be there.  Returns its index."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    return dev
+
+
+def _stream_on(stream, device):
+    """The address of the stream that a call runs on: `stream`, or the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
+    return stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """A new contiguous tensor that belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 _MAXI32 = 2**31 - 1
@@ -711,30 +730,31 @@ def _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, bet
     if h.dim() != 2:
         raise ValueError("h must be 2-D (tokens x width)")
     dev = _current(h, "h")
-    T, d = h.shape
-    J = poet_joint(min(d, _MAXI32), _dtype_of(h, "h"), 1 if post_norm and o is not None else 0, GATE_NONE, gate_act, 0,
-                   gate_rows, alpha, beta, eps, None, None)
-    ph = _operand(h, "h", (T, d), h.dtype, dev)
-    po = (None, 0)
-    pg = (None, 0)
+    shape = T, d = h.shape
+    t = h.dtype
+    ph, ldh = _operand(h, "h", shape, t, dev)
+    kind, po, ldo, pg, ldg, pq, pn = GATE_NONE, None, 0, None, 0, None, None
     if o is not None:
-        po = _operand(o, "o", (T, d), h.dtype, dev)
+        po, ldo = _operand(o, "o", shape, t, dev)
         if w_post is not None:
-            J.w_post = _operand(w_post, "w_post", (d,), torch.float32, dev)[0]
+            pq = _operand(w_post, "w_post", (d,), torch.float32, dev, False)[0]
         if gate is not None:
             if gate_rows < 1:
                 raise ValueError("gate_rows must be at least 1")
             G = -(-T // gate_rows)
-            J.gate = GATE_CHANNEL if gate.dim() == 2 else GATE_ROW
-            if gate.dim() == 1:
-                pg = (_operand(gate, "gate", (G,), h.dtype, dev, rows=False)[0], 1)
+            if gate.dim() == 2:
+                kind = GATE_CHANNEL
+                pg, ldg = _operand(gate, "gate", (G, d), t, dev)
             else:
-                pg = _operand(gate, "gate", (G, d), h.dtype, dev)
+                kind = GATE_ROW
+                pg, ldg = _operand(gate, "gate", (G,), t, dev, False)[0], 1
     elif gate is not None or w_post is not None:
         raise ValueError("a gate and w_post need o")
     if w_pre is not None:
-        J.w_pre = _operand(w_pre, "w_pre", (d,), torch.float32, dev)[0]
-    return J, dev, T, d, po, ph, pg
+        pn = _operand(w_pre, "w_pre", (d,), torch.float32, dev, False)[0]
+    J = poet_joint(d if d <= _MAXI32 else _MAXI32, _dtype_of(h, "h"), 1 if post_norm and o is not None else 0, kind,
+                   gate_act, 0, gate_rows, alpha, beta, eps, pq, pn)
+    return J, dev, shape, t, po, ldo, ph, ldh, pg, ldg
 
 
 def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, pre_norm=True, gate_act=GATE_LINEAR,
@@ -744,19 +764,27 @@ def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, p
     o, h: T x d (float32 or bfloat16, rows contiguous).  gate: G x d or G values, G = ceil(T / gate_rows),
     shared by gate_rows consecutive tokens.  w_post, w_pre: float32 [d] or None (gains of 1).  post_norm=False
     takes o as it is; pre_norm=False leaves n out (None).  o=None: n = rmsnorm(h) w_pre alone (h' is None).
-    h_out and n are allocated where they are not given."""
-    J, dev, T, d, po, ph, pg = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps)
+    h_out and n are allocated where they are not given.  stream: the stream to run on (None: the current one);
+    what is allocated belongs to it."""
+    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows,
+                                                         alpha, beta, eps)
     if o is None and (h_out is not None or not pre_norm):
         raise ValueError("without o there is only n")
-    if o is not None and h_out is None:
-        h_out = torch.empty(T, d, dtype=h.dtype, device=dev)
     if not pre_norm and (n is not None or w_pre is not None):
         raise ValueError("n and w_pre need pre_norm")
-    if pre_norm and n is None:
-        n = torch.empty(T, d, dtype=h.dtype, device=dev)
-    pho = _operand(h_out, "h_out", (T, d), h.dtype, dev) if o is not None else (None, 0)
-    pn = _operand(n, "n", (T, d), h.dtype, dev) if pre_norm else (None, 0)
-    _check(lib().poet_joint_forward(ctypes.byref(J), *po, *ph, *pg, T, *pho, *pn, _stream(stream)))
+    st = _stream_on(stream, dev)
+    pho, ldho, pn, ldn = None, 0, None, 0
+    if h_out is not None:
+        pho, ldho = _operand(h_out, "h_out", shape, t, dev)
+    elif o is not None:
+        h_out = _new(shape, t, dev, stream)
+        pho, ldho = h_out.data_ptr(), shape[1]
+    if n is not None:
+        pn, ldn = _operand(n, "n", shape, t, dev)
+    elif pre_norm:
+        n = _new(shape, t, dev, stream)
+        pn, ldn = n.data_ptr(), shape[1]
+    _check(lib().poet_joint_forward(ctypes.byref(J), po, ldo, ph, ldh, pg, ldg, shape[0], pho, ldho, pn, ldn, st))
     return h_out, n
 
 
@@ -771,38 +799,43 @@ def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_
                    dw_pre=None, ws=None, stream=None):
     """(dh, d_o, dgate, dw_post, dw_pre) of joint_forward for the gradients dh_out of h' and dn of n (either may
     be None).  o, gate and the options are the forward's, h_out its result (h where o is None).  Gradients of
-    what the joint does not have are None; the others are allocated where they are not given (ws too)."""
-    J, dev, T, d, po, ph, pg = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps)
-    t = h_out.dtype
+    what the joint does not have are None; the others are allocated where they are not given (ws too).  Two
+    calls that may run at the same time need a ws each."""
+    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows,
+                                                         alpha, beta, eps)
+    d = shape[1]
     if dn is None and w_pre is not None:
         raise ValueError("w_pre needs dn")
-    pd = _operand(dh_out, "dh_out", (T, d), t, dev) if dh_out is not None else (None, 0)
-    pn = _operand(dn, "dn", (T, d), t, dev) if dn is not None else (None, 0)
-    if dh is None:
-        dh = torch.empty(T, d, dtype=t, device=dev)
-    if o is not None and d_o is None:
-        d_o = torch.empty(T, d, dtype=t, device=dev)
-    if gate is not None and dgate is None:
-        dgate = torch.empty(gate.shape, dtype=t, device=dev)
-    if w_post is not None and dw_post is None:
-        dw_post = torch.empty(d, dtype=torch.float32, device=dev)
-    if w_pre is not None and dw_pre is None:
-        dw_pre = torch.empty(d, dtype=torch.float32, device=dev)
     for name, have, want in (("d_o", d_o, o), ("dgate", dgate, gate), ("dw_post", dw_post, w_post),
                              ("dw_pre", dw_pre, w_pre)):
         if have is not None and want is None:
             raise ValueError(f"{name} is the gradient of something this joint does not have")
-    pdh = _operand(dh, "dh", (T, d), t, dev)
-    pdo = _operand(d_o, "d_o", (T, d), t, dev) if d_o is not None else (None, 0)
-    pdg = (None, 0)
-    if dgate is not None:
-        pdg = _operand(dgate, "dgate", gate.shape, t, dev, rows=gate.dim() == 2)
-    pwq = _operand(dw_post, "dw_post", (d,), torch.float32, dev)[0] if dw_post is not None else None
-    pwn = _operand(dw_pre, "dw_pre", (d,), torch.float32, dev)[0] if dw_pre is not None else None
+    st = _stream_on(stream, dev)
+
+    def result(x, name, shape, dtype, of):
+        """A gradient (x, or a new one where `of` is there), its address and row stride."""
+        if x is not None:
+            return (x, *_operand(x, name, shape, dtype, dev, len(shape) == 2))
+        if of is None:
+            return None, None, 0
+        x = _new(shape, dtype, dev, stream)
+        return x, x.data_ptr(), shape[-1]
+
+    pd, ldd = _operand(dh_out, "dh_out", shape, t, dev) if dh_out is not None else (None, 0)
+    pn, ldn = _operand(dn, "dn", shape, t, dev) if dn is not None else (None, 0)
+    dh, pdh, lddh = result(dh, "dh", shape, t, h_out)
+    d_o, pdo, lddo = result(d_o, "d_o", shape, t, o)
+    dgate, pdg, lddg = result(dgate, "dgate", gate.shape if gate is not None else None, t, gate)
+    if gate is not None and gate.dim() == 1:
+        lddg = 1
+    dw_post, pwq, _ = result(dw_post, "dw_post", (d,), torch.float32, w_post)
+    dw_pre, pwn, _ = result(dw_pre, "dw_pre", (d,), torch.float32, w_pre)
     if ws is None:
-        ws = torch.empty(max(lib().poet_joint_workspace_bytes(ctypes.byref(J), T), 1), dtype=torch.uint8, device=dev)
-    _check(lib().poet_joint_backward(ctypes.byref(J), *po, *ph, *pg, *pd, *pn, T, *pdh, *pdo, *pdg, pwq, pwn,
-                                     _ptr(ws), ws.numel(), _stream(stream)))
+        ws = _new((max(lib().poet_joint_workspace_bytes(ctypes.byref(J), shape[0]), 1),), torch.uint8, dev, stream)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, not on cuda:{dev}")
+    _check(lib().poet_joint_backward(ctypes.byref(J), po, ldo, ph, ldh, pg, ldg, pd, ldd, pn, ldn, shape[0], pdh, lddh,
+                                     pdo, lddo, pdg, lddg, pwq, pwn, ws.data_ptr(), ws.nbytes, st))
     return dh, d_o, dgate, dw_post, dw_pre
 
 
@@ -814,7 +847,20 @@ def _logits(x, name="logits"):
         raise ValueError(f"{name} must be 2-D (tokens x vocabulary)")
     dev = _current(x, name)
     T, V = x.shape
-    return (dev, _dtype_of(x, name), T, min(V, _MAXI32)) + _operand(x, name, (T, V), x.dtype, dev)
+    p, ld = _operand(x, name, x.shape, x.dtype, dev)
+    return dev, _dtype_of(x, name), T, (V if V <= _MAXI32 else _MAXI32), p, ld
+
+
+def _per_row(x, name, T, dtype, dev):
+    """The address of one value per row (None: not there)."""
+    return None if x is None else _operand(x, name, (T,), dtype, dev, False)[0]
+
+
+def _matrix(x, logits, dev, stream):
+    """(dlogits, address, row stride): x, or a new matrix of the logits' shape and type."""
+    if x is None:
+        x = _new(logits.shape, logits.dtype, dev, stream)
+    return (x, *_operand(x, "dlogits", logits.shape, logits.dtype, dev))
 
 
 def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, saved=None, stream=None):
@@ -824,35 +870,37 @@ def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, save
     alternatives to list (0: none).  entropy=False leaves the entropy out (None).  saved: float32 [T, 4],
     what token_logprobs_grad reads (allocated where it is not given)."""
     dev, dt, T, V, px, ld = _logits(logits)
-    logp = pt = None
-    if tokens is not None:
-        pt = _operand(tokens, "tokens", (T,), torch.int32, dev, rows=False)[0]
-        logp = torch.empty(T, dtype=torch.float32, device=dev)
-    H = torch.empty(T, dtype=torch.float32, device=dev) if entropy else None
-    top = topl = None
+    pt = _per_row(tokens, "tokens", T, torch.int32, dev)
+    st = _stream_on(stream, dev)
+    logp = H = top = topl = pl = ph = ptop = ptl = None
+    if pt is not None:
+        logp = _new((T,), torch.float32, dev, stream)
+        pl = logp.data_ptr()
+    if entropy:
+        H = _new((T,), torch.float32, dev, stream)
+        ph = H.data_ptr()
     if topk > 0:
-        top = torch.empty(T, topk, dtype=torch.int32, device=dev)
-        topl = torch.empty(T, topk, dtype=torch.float32, device=dev)
+        top = _new((T, topk), torch.int32, dev, stream)
+        topl = _new((T, topk), torch.float32, dev, stream)
+        ptop, ptl = top.data_ptr(), topl.data_ptr()
     if saved is None:
-        saved = torch.empty(T, 4, dtype=torch.float32, device=dev)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
-    _check(lib().poet_token_logprobs(px, ld, dt, T, V, scale, pt, topk, _ptr(logp), _ptr(H), _ptr(top), _ptr(topl), ps,
-                                     _stream(stream)))
+        saved = _new((T, 4), torch.float32, dev, stream)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    _check(lib().poet_token_logprobs(px, ld, dt, T, V, scale, pt, topk, pl, ph, ptop, ptl, ps, st))
     return logp, H, top, topl, saved
 
 
 def token_logprobs_grad(logits, tokens, saved, dlogp=None, dentropy=None, *, scale=1.0, dlogits=None, stream=None):
     """dlogits for the gradients dlogp and dentropy (float32 [T], either may be None) of token_logprobs's
-    results; saved: the forward's (with its entropy where dentropy is given).  dlogits may be logits."""
+    results; saved: the forward's.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
-    pt = _operand(tokens, "tokens", (T,), torch.int32, dev, rows=False)[0] if tokens is not None else None
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
-    pl = _operand(dlogp, "dlogp", (T,), torch.float32, dev, rows=False)[0] if dlogp is not None else None
-    pe = _operand(dentropy, "dentropy", (T,), torch.float32, dev, rows=False)[0] if dentropy is not None else None
-    if dlogits is None:
-        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
-    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev)
-    _check(lib().poet_token_logprobs_grad(px, ld, dt, T, V, scale, pt, ps, pl, pe, pd, ldd, _stream(stream)))
+    pt = _per_row(tokens, "tokens", T, torch.int32, dev)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    pl = _per_row(dlogp, "dlogp", T, torch.float32, dev)
+    pe = _per_row(dentropy, "dentropy", T, torch.float32, dev)
+    st = _stream_on(stream, dev)
+    dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
+    _check(lib().poet_token_logprobs_grad(px, ld, dt, T, V, scale, pt, ps, pl, pe, pd, ldd, st))
     return dlogits
 
 
@@ -860,8 +908,8 @@ def _teacher(teacher_tokens, teacher_values, T, dev):
     if teacher_tokens.dim() != 2:
         raise ValueError("teacher_tokens must be 2-D (tokens x entries)")
     K = teacher_tokens.shape[1]
-    return (_operand(teacher_tokens, "teacher_tokens", (T, K), torch.int32, dev, rows=False)[0],
-            _operand(teacher_values, "teacher_values", (T, K), torch.float32, dev, rows=False)[0], min(K, _MAXI32))
+    return (_operand(teacher_tokens, "teacher_tokens", (T, K), torch.int32, dev, False)[0],
+            _operand(teacher_values, "teacher_values", (T, K), torch.float32, dev, False)[0], min(K, _MAXI32))
 
 
 def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tail=False, scale=1.0, dloss=None,
@@ -874,16 +922,17 @@ def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tai
     float32 [T], None = 1), formed in the same pass; otherwise None.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
-    pw = _operand(dloss, "dloss", (T,), torch.float32, dev, rows=False)[0] if dloss is not None else None
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    pw = _per_row(dloss, "dloss", T, torch.float32, dev)
+    st = _stream_on(stream, dev)
+    loss = _new((T,), torch.float32, dev, stream)
     if saved is None:
-        saved = torch.empty(T, 4, dtype=torch.float32, device=dev)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
-    if grad and dlogits is None:
-        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
-    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev) if dlogits is not None else (None, 0)
+        saved = _new((T, 4), torch.float32, dev, stream)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    pd, ldd = None, 0
+    if grad or dlogits is not None:
+        dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
     _check(lib().poet_distill_topk(px, ld, dt, T, V, scale, pt, pv, K, value_scale, 1 if tail else 0, pw,
-                                   loss.data_ptr(), ps, pd, ldd, _stream(stream)))
+                                   loss.data_ptr(), ps, pd, ldd, st))
     return loss, dlogits, saved
 
 
@@ -892,11 +941,10 @@ def distill_topk_grad(logits, teacher_tokens, teacher_values, saved, dloss=None,
     """dlogits = the gradient of sum dloss * loss, from the forward's saved.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
-    pw = _operand(dloss, "dloss", (T,), torch.float32, dev, rows=False)[0] if dloss is not None else None
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, rows=False)[0]
-    if dlogits is None:
-        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
-    pd, ldd = _operand(dlogits, "dlogits", (T, V), logits.dtype, dev)
+    pw = _per_row(dloss, "dloss", T, torch.float32, dev)
+    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    st = _stream_on(stream, dev)
+    dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
     _check(lib().poet_distill_topk_grad(px, ld, dt, T, V, scale, pt, pv, K, value_scale, 1 if tail else 0, ps, pw, pd,
-                                        ldd, _stream(stream)))
+                                        ldd, st))
     return dlogits
