@@ -2,17 +2,21 @@
 // and top alternatives, distillation from a teacher's top logits, and their
 // gradients.
 //
-// A row of V logits is worked on by a cluster of C CTAs (C = 1 where there are
-// rows enough to fill the GPU), each with a contiguous slice.  One pass over
-// the slice keeps, per thread, the running maximum m, s = sum exp(c (x - m))
-// and t = sum exp(c (x - m)) c (x - m); these are joined through shuffles,
-// shared memory and the cluster's distributed shared memory, always in one
-// order.  c = scale log2(e), so an exponential is one ex2; differences to the
-// maximum are formed before they are scaled, so neither large logits nor masks
-// of the type's lowest value lose anything.
+// One pass over a row of V logits keeps, per thread, the running maximum m,
+// s = sum exp(c (x - m)) and t = sum exp(c (x - m)) c (x - m); these are joined
+// through shuffles, shared memory and the cluster's distributed shared memory,
+// always in one order.  c = scale log2(e), so an exponential is one ex2;
+// differences to the maximum are formed before they are scaled, so neither large
+// logits nor masks of the type's lowest value lose anything.
 //
-// HBM-bound: the forward reads the logits once.  The fused loss + gradient
-// reads them again in its second pass, from L2.
+// The forward operators are persistent: a CTA (or, with few rows, a cluster of
+// CTAs, each with a contiguous slice) works through rows, and one warp of it
+// streams their 16-byte vectors through a ring of stages in shared memory by
+// bulk copies, so that the next rows are on their way while a row's sums are
+// joined, its alternatives selected or its gradient written.  What bounds them:
+// HBM (each logit is read once, each gradient written once) and, close behind,
+// the exponential (16 a clock and SM: 73 % of the time that HBM needs for a
+// bf16 logit) and instruction issue, hence the arithmetic in pairs.
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -28,9 +32,8 @@ constexpr int MAX_V = 2097152;
 constexpr int MAX_K = 128;
 constexpr int MAX_CLUSTER = 8;
 constexpr int SLICE = 262144;  // most columns of one CTA
-constexpr int NT = 256;
-constexpr int NW = NT / 32;
-constexpr int CAND = 1024;     // candidates kept at once by the selection
+constexpr int NT = 256;        // threads of the element-wise gradients
+constexpr int CAND = 2048;     // candidates kept at once by the selection
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -1e30f;
 
@@ -39,6 +42,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
 // The aligned part of a row slice: elements [lo, lo + head) one by one, then
 // `nv` 16-byte vectors, then elements [tail0, hi) one by one.
@@ -58,7 +62,11 @@ __device__ __forceinline__ Slice<T> slice_of(const T *p, int V, int rank, int si
   int head = int(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T));
   if (head > V) head = V;
   const int nv = (V - head) / E;
-  const int b0 = int(int64_t(nv) * rank / size), b1 = int(int64_t(nv) * (rank + 1) / size);
+  int b0 = 0, b1 = nv;
+  if (size > 1) {  // nv * size < 2^32: V <= MAX_V, size <= 512
+    b0 = int(unsigned(nv) * unsigned(rank) / unsigned(size));
+    b1 = int(unsigned(nv) * unsigned(rank + 1) / unsigned(size));
+  }
   s.lo = rank == 0 ? 0 : head + b0 * E;
   s.head = rank == 0 ? head : 0;
   s.nv = b1 - b0;
@@ -67,50 +75,50 @@ __device__ __forceinline__ Slice<T> slice_of(const T *p, int V, int rank, int si
   return s;
 }
 
-// The running sums of some logits of a row.
+// The running sums of some logits of a row, in pairs, relative to a base that
+// follows their maximum: it is moved only when an exponent would pass RISE, which
+// after a thread's first logits is rare, and the sums' relative errors do not
+// depend on it.
+constexpr float RISE = 8.f;
 struct Run {
-  float m, s, t;
-  __device__ __forceinline__ void clear() { m = -INFINITY; s = 0.f; t = 0.f; }
-  // Move to maximum mx >= m.
-  __device__ __forceinline__ void raise(float mx, float c) {
-    const float base = mx == -INFINITY ? 0.f : mx;
-    const float d = fmaxf((m - base) * c, LOWEST);
-    const float f = ex2((m - base) * c);
-    t = fmaf(s, d, t) * f;
-    s *= f;
-    m = mx;
+  float m, b;  // the largest, the base
+  float2 s, t;
+  __device__ __forceinline__ void clear() { m = b = -INFINITY; s = t = both(0.f); }
+  __device__ __forceinline__ float base() const { return b == -INFINITY ? 0.f : b; }
+  __device__ __forceinline__ void rebase(float to, float c) {  // to >= b
+    const float d = (b - (to == -INFINITY ? 0.f : to)) * c;
+    const float2 f = both(ex2(d));
+    t = mul2(fma2(s, both(fmaxf(d, LOWEST)), t), f);
+    s = mul2(s, f);
+    b = to;
   }
-  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
-  template <bool ENT>
-  __device__ __forceinline__ void add(float x, float b, float c) {
-    const float d = (x - b) * c;
-    const float e = ex2(d);
-    s += e;
-    if (ENT) t = fmaf(e, fmaxf(d, LOWEST), t);
+  // Takes mx into the maximum; call before adding logits up to mx.
+  __device__ __forceinline__ void see(float mx, float c) {
+    m = fmaxf(m, mx);
+    if ((mx - b) * c > RISE) rebase(mx, c);
   }
-  __device__ __forceinline__ void join(float om, float os, float ot, float c) {
-    Run o{om, os, ot};
-    const float mx = fmaxf(m, om);
-    raise(mx, c);
-    o.raise(mx, c);
-    s += o.s;
-    t += o.t;
-  }
-  __device__ __forceinline__ void join_warp(float c) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o),
-                  ot = __shfl_xor_sync(0xffffffffu, t, o);
-      // both sides of a pair join in the same order, so that they agree to the bit
-      if ((threadIdx.x & o) == 0) {
-        join(om, os, ot, c);
-      } else {
-        Run a{om, os, ot};
-        a.join(m, s, t, c);
-        *this = a;
-      }
+  // Adds exp(d) and exp(d) d; LOW: some d may be -inf.
+  template <bool ENT, bool LOW>
+  __device__ __forceinline__ void add(float2 x, float2 minus_base, float2 c) {
+    float2 d = mul2(add2(x, minus_base), c);
+    const float2 e = ex2(d);
+    s = add2(s, e);
+    if (ENT) {
+      if (LOW) d = make_float2(fmaxf(d.x, LOWEST), fmaxf(d.y, LOWEST));
+      t = fma2(e, d, t);
     }
   }
+  __device__ __forceinline__ void add1(float x, float c) {
+    const float d = (x - base()) * c, e = ex2(d);
+    s.x += e;
+    t.x = fmaf(e, fmaxf(d, LOWEST), t.x);
+  }
+};
+
+// The joined sums of some logits.
+struct Sums {
+  float m, s, t;
+  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
 };
 
 // Order of logits as unsigned integers (-0 and +0 equal; larger is larger).
@@ -123,71 +131,566 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 }
 constexpr uint32_t KEY_MASKED = 0x007fffffu;  // key_of(-inf)
 
+// Joins the sums that groups of 2^LOG lanes hold; every lane of a group gets the result.
+template <int LOG>
+__device__ __forceinline__ Sums join_lanes(Sums a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 1 << LOG >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float d = (a.m - (m == -INFINITY ? 0.f : m)) * c, f = ex2(d);
+  float s = a.s * f, t = fmaf(a.s, fmaxf(d, LOWEST), a.t) * f;
+#pragma unroll
+  for (int o = 1 << LOG >> 1; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  return {m, s, t};
+}
+__device__ __forceinline__ Sums join_warp(Run &r, float c) {
+  const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(r.m)));
+  r.rebase(m, c);
+  float v[2] = {r.s.x + r.s.y, r.t.x + r.t.y};
+  row_sum<2>(v, nullptr, 1, 0, 0, 32);
+  return {m, v[0], v[1]};
+}
+
+// A 16-byte vector of logits: its extremes (NaN ignored) and its pairs.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T *p, float (&f)[16 / sizeof(T)]) {
-  RowVec<T, 16 / sizeof(T)> v;
-  v.load(p);
-  v.get(f);
+struct Vec;
+template <>
+struct Vec<bf16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t MASKED = 0xff80ff80u;
+  using Top = __nv_bfloat162;
+  static __device__ __forceinline__ Top word(uint32_t w) { return *reinterpret_cast<const Top *>(&w); }
+  static __device__ __forceinline__ Top largest(const uint4 &v) {
+    return __hmax2(__hmax2(word(v.x), word(v.y)), __hmax2(word(v.z), word(v.w)));
+  }
+  static __device__ __forceinline__ Top smallest(const uint4 &v) {
+    return __hmin2(__hmin2(word(v.x), word(v.y)), __hmin2(word(v.z), word(v.w)));
+  }
+  static __device__ __forceinline__ Top larger(Top a, Top b) { return __hmax2(a, b); }
+  static __device__ __forceinline__ Top smaller(Top a, Top b) { return __hmin2(a, b); }
+  static __device__ __forceinline__ float top(Top a) { return fmaxf(__low2float(a), __high2float(a)); }
+  static __device__ __forceinline__ float bottom(Top a) { return fminf(__low2float(a), __high2float(a)); }
+  static __device__ __forceinline__ void get(const uint4 &v, float2 (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 put(const float2 (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __float22bfloat162_rn(x[i]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // -inf in place of the elements whose bit is set
+  static __device__ __forceinline__ void mask(uint4 &v, unsigned bits) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((bits >> (2 * i)) & 1u) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+      if ((bits >> (2 * i + 1)) & 1u) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int E = 4;
+  static constexpr uint32_t MASKED = 0xff800000u;
+  using Top = float;
+  static __device__ __forceinline__ float f(uint32_t w) { return __uint_as_float(w); }
+  static __device__ __forceinline__ Top largest(const uint4 &v) {
+    return fmaxf(fmaxf(f(v.x), f(v.y)), fmaxf(f(v.z), f(v.w)));
+  }
+  static __device__ __forceinline__ Top smallest(const uint4 &v) {
+    return fminf(fminf(f(v.x), f(v.y)), fminf(f(v.z), f(v.w)));
+  }
+  static __device__ __forceinline__ Top larger(Top a, Top b) { return fmaxf(a, b); }
+  static __device__ __forceinline__ Top smaller(Top a, Top b) { return fminf(a, b); }
+  static __device__ __forceinline__ float top(Top a) { return a; }
+  static __device__ __forceinline__ float bottom(Top a) { return a; }
+  static __device__ __forceinline__ void get(const uint4 &v, float2 (&x)[2]) {
+    x[0] = make_float2(f(v.x), f(v.y));
+    x[1] = make_float2(f(v.z), f(v.w));
+  }
+  static __device__ __forceinline__ uint4 put(const float2 (&x)[2]) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+  }
+  static __device__ __forceinline__ void mask(uint4 &v, unsigned bits) {
+    if (bits & 1u) v.x = MASKED;
+    if (bits & 2u) v.y = MASKED;
+    if (bits & 4u) v.z = MASKED;
+    if (bits & 8u) v.w = MASKED;
+  }
+};
+
+// ------------------------------------------------------------------ the stream of rows
+
+constexpr int U = 4;             // vectors of a thread in one stage
+constexpr int MAX_STAGES = 12;
+// CTAs that share an SM: three of eight computing warps where the registers allow it.
+template <int NW>
+constexpr int per_sm(bool lean) { return NW == 8 ? (lean ? 3 : 2) : 6; }
+constexpr int BAR = 1;           // the named barrier of the warps that compute
+constexpr uint64_t TIMEOUT_NS = 4000000000ull;
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t peer_at(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(b)) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_peer(uint64_t *b, int rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_at(smem_at(b), rank)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t at, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(at), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase of this parity.  Every wait ends: after TIMEOUT_NS it
+// records ERR_TIMEOUT, and from then on the CTA's waits return at once (its
+// results are void, and the producer issues nothing more).
+__device__ __noinline__ bool bar_wait_long(uint32_t at, uint32_t parity, volatile int *abort, unsigned *errword) {
+  const uint64_t t0 = now_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (bar_try(at, parity)) return true;
+    if ((it & 63) == 0) {
+      if (*abort) return false;
+      if (now_ns() - t0 > TIMEOUT_NS) {
+        atomicOr(errword, unsigned(ERR_TIMEOUT));
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *errword) {
+  const uint32_t at = smem_at(b);
+  return bar_try(at, parity) || bar_wait_long(at, parity, abort, errword);
+}
+
+// The ring's barriers and the exchange of the cluster's CTAs.
+struct Pipe {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t join, gather;     // the cluster's exchanges of a row
+  uint64_t tfull[2], tempty[2];  // the teacher's buffers
+  float4 part[2][MAX_CLUSTER];
+  float4 warp[2][8];
+  int abort;
+};
+template <int NW>
+__device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, cg::cluster_group &cl) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      bar_init(&P.full[i], 1);
+      bar_init(&P.empty[i], NW);
+    }
+    bar_init(&P.join, size);
+    bar_init(&P.gather, size);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&P.tfull[i], 1);
+      bar_init(&P.tempty[i], NW);
+    }
+    P.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (size > 1) cl.sync();
+  else __syncthreads();
+}
+
+// A place in the ring.
+struct Spot {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// The producer: one thread copies the vectors of every row's slice, NW * 32 * U
+// at a time, into the ring; `passes` times each row (a second time where a row
+// does not fit the ring and is read again for its gradient).  live(row): whether
+// the row is read at all (the whole warp calls it).
+template <typename T, int NW, typename F>
+__device__ void produce(Pipe &P, const unsigned char *ring, int stages, const void *x0, int64_t ld, int V, int64_t T_rows,
+                        int64_t first, int64_t step, int rank, int size, bool twice, unsigned *errword, F live) {
+  constexpr int SV = NW * 32 * U;
+  Spot at;
+  int64_t issued = 0;
+  bool ok = true;
+  for (int64_t row = first; row < T_rows && ok; row += step) {
+    if (!live(row)) continue;
+    const T *x = static_cast<const T *>(x0) + row * ld;
+    const Slice<T> sl = slice_of(x, V, rank, size);
+    const T *body = x + sl.lo + sl.head;
+    if ((threadIdx.x & 31) == 0) {
+      const int nst = (sl.nv + SV - 1) / SV;
+      const int passes = twice && nst > stages ? 2 : 1;
+      for (int p = 0; p < passes && ok; ++p)
+        for (int k = 0; k < nst; ++k) {
+          if (!bar_wait(&P.empty[at.st], at.ph ^ 1, &P.abort, errword)) {
+            ok = false;
+            break;
+          }
+          const int n = min(sl.nv - k * SV, SV);
+          const uint32_t bar = smem_at(&P.full[at.st]), bytes = uint32_t(n) * 16;
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           smem_at(ring) + at.st * (SV * 16)),
+                       "l"(body + int64_t(k) * SV * Vec<T>::E), "r"(bytes), "r"(bar)
+                       : "memory");
+          ++issued;
+          at.next(stages);
+        }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+  }
+  // after an abort: the copies in flight, with a limit
+  if (!ok && (threadIdx.x & 31) == 0) {
+    const uint64_t t0 = now_ns();
+    for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+      while (!bar_try(smem_at(&P.full[k % stages]), uint32_t(k / stages) & 1) && now_ns() - t0 < TIMEOUT_NS) {
+      }
+  }
+  __syncwarp();
+}
+
+template <int NW>
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(NW * 32) : "memory");
+}
+
+// A stage's vectors of this thread; those behind the slice's end are masked.
+template <typename T, int NW>
+__device__ __forceinline__ void read_stage(uint4 (&v)[U], const unsigned char *ring, int st, int left) {
+  const uint4 *p = reinterpret_cast<const uint4 *>(ring + st * (NW * 32 * U * 16)) + threadIdx.x;
+  if (left >= NW * 32 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = p[u * NW * 32];
+  } else {
+    constexpr uint32_t M = Vec<T>::MASKED;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = u * NW * 32 + int(threadIdx.x) < left ? p[u * NW * 32] : make_uint4(M, M, M, M);
+  }
+}
+
+// Adds a thread's vectors to its sums; returns their largest logit.
+template <typename T, bool ENT>
+__device__ __forceinline__ float add_vectors(Run &r, const uint4 (&v)[U], float c) {
+  using X = Vec<T>;
+  typename X::Top hi = X::largest(v[0]);
+#pragma unroll
+  for (int u = 1; u < U; ++u) hi = X::larger(hi, X::largest(v[u]));
+  const float mx = X::top(hi);
+  r.see(mx, c);
+  bool low = false;
+  if (ENT) {  // may an exponent be -inf?
+    typename X::Top lo = X::smallest(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) lo = X::smaller(lo, X::smallest(v[u]));
+    low = !((X::bottom(lo) - r.base()) * c > LOWEST);
+  }
+  const float2 mb = both(-r.base()), c2 = both(c);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float2 x[X::E / 2];
+    X::get(v[u], x);
+    if (ENT && low) {
+#pragma unroll
+      for (int i = 0; i < X::E / 2; ++i) r.add<ENT, true>(x[i], mb, c2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < X::E / 2; ++i) r.add<ENT, false>(x[i], mb, c2);
+    }
+  }
+  return mx;
+}
+
+// Joins the threads' sums of a row: all threads of the CTA (and of the cluster)
+// get the row's sums.  `par` is the row's parity among those that this CTA
+// joins: the buffers alternate, and a buffer is written again only after the
+// barrier (the exchange) of the row between.  *floor: a value of each thread's;
+// the CTA's smallest on return.
+template <int NW>
+__device__ __forceinline__ Sums join_row(Pipe &P, Run &r, float c, int par, int rank, int size, unsigned *errword,
+                                         float *floor, bool one_warp = false) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float low = floor ? of_key(__reduce_min_sync(0xffffffffu, key_of(*floor))) : 0.f;
+  const Sums w = join_warp(r, c);
+  if (lane == 0) P.warp[par][warp] = make_float4(w.m, w.s, w.t, low);
+  warps_sync<NW>();
+  if (one_warp && warp != 0) return {0.f, 0.f, 0.f};
+  const float4 f = P.warp[par][lane % NW];
+  Sums all = join_lanes<NW == 8 ? 3 : 1>({f.x, f.y, f.z}, c);
+  if (floor) {
+    float m = f.w;
+#pragma unroll
+    for (int o = NW / 2; o > 0; o >>= 1) m = fminf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    *floor = m;
+  }
+  if (size > 1) {
+    if (warp == 0 && lane < size) {
+      const uint32_t to = peer_at(smem_at(&P.part[par][rank]), lane);
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(all.m), "f"(all.s), "f"(all.t),
+                   "f"(0.f)
+                   : "memory");
+      bar_arrive_peer(&P.join, lane);
+    }
+    bar_wait(&P.join, par, &P.abort, errword);
+    const int q = lane % MAX_CLUSTER;
+    const float4 g = q < size ? P.part[par][q] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    all = join_lanes<3>({g.x, g.y, g.z}, c);
+  }
+  return all;
+}
+
+// The ragged ends of a slice, at most E - 1 elements each, one per lane of the
+// first warp, added to its sums.
+template <typename T>
+__device__ __forceinline__ void add_ends(Run &r, float xh, float xt, float c) {
+  const float mx = fmaxf(xh, xt);
+  r.see(mx, c);
+  r.add1(xh, c);
+  r.add1(xt, c);
 }
 
 // ------------------------------------------------------------------ selection of the largest
 
-struct SelectSmem {
+// Shared memory of the selection.  The logits of a thread in one stage are a
+// group; keys holds every group's largest (group k * NW * 32 + thread of stage
+// k), ends those of the elements before and behind the slice's vectors.
+struct Select {
   unsigned long long cand[CAND];
   unsigned long long best[MAX_K];
   unsigned list[256];
+  unsigned counts[2][8];
   unsigned n, m;
-  unsigned count;
+  float ends[2];
 };
 
-// Number of items for which the predicate holds over the CTA's threads.
-__device__ __forceinline__ unsigned cta_sum(unsigned v, unsigned *cell) {
+// The sum of a count over the CTA; one barrier, buffers alternate.
+template <int NW>
+__device__ __forceinline__ unsigned cta_count(Select &S, unsigned v, int &flip) {
   v = __reduce_add_sync(0xffffffffu, v);
-  if (threadIdx.x == 0) *cell = 0;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0 && v) atomicAdd(cell, v);
-  __syncthreads();
-  const unsigned total = *cell;
-  __syncthreads();
+  if ((threadIdx.x & 31) == 0) S.counts[flip][threadIdx.x >> 5] = v;
+  warps_sync<NW>();
+  unsigned total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) total += S.counts[flip][w];
+  flip ^= 1;
   return total;
 }
 
-// A bound with between `least` and `most` items at or above it, by bisection of
-// the 64-bit order (which has no ties, so it ends); 0 if there are no more than
-// `most` items.  count(b): the thread's number of items >= b.
-template <typename F>
-__device__ unsigned long long bound_for(unsigned least, unsigned most, unsigned long long hi, unsigned *cell, F count) {
-  unsigned long long lo = 0;  // count(lo) > most, count(hi) < least
-  for (;;) {
-    const unsigned long long mid = lo + (hi - lo) / 2;
-    const unsigned c = cta_sum(count(mid), cell);
-    if (c < least) hi = mid;
-    else if (c > most) lo = mid;
-    else return mid;
-    if (hi - lo <= 1) return lo;  // not reached: orders are distinct
-  }
+__device__ __forceinline__ unsigned long long order_of(float x, unsigned index) {
+  return (static_cast<unsigned long long>(key_of(x)) << 32) | (0xffffffffu - index);
 }
 
-// From n candidates in S.cand (distinct) the K largest, in falling order, to
-// S.best (0 where there are fewer); n <= CAND.
-__device__ void rank_candidates(SelectSmem &S, unsigned n, unsigned K) {
-  for (unsigned i = threadIdx.x; i < K; i += NT)
+// The K largest logits of a slice (equal ones: the lower index first), in
+// falling order, as order_of, to S.best, 0 where there are fewer; -inf is never
+// among them.  `floor`: the smallest of the threads' maxima, `top`: the slice's
+// largest logit; no NaN.
+//
+// The K-th largest of the groups' maxima is a bound that at least K logits
+// reach and few others: one between it and the `most`-th largest is found by
+// bisection, first of values, then of the order of floats; then only the
+// groups that reach it are read again (from L2).  Where equal logits or a few
+// crowded groups leave too many candidates, the exact bound is found by
+// bisection over the slice's elements.
+template <typename T, int NW>
+__device__ void select_largest(Select &S, const float *keys, const T *x, const Slice<T> &sl, int nst, unsigned K,
+                               float floor, float top) {
+  constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E;
+  const int tid = threadIdx.x;
+  const T *body = x + sl.lo + sl.head;
+  int flip = 0;
+  const unsigned most = K + K / 2 < 32 ? 32 : K + K / 2;  // <= 192 < 256
+  auto groups_at = [&](float b) {
+    unsigned n = 0;
+    for (int k = 0; k < nst; ++k) n += keys[k * G + tid] >= b;
+    if (tid == 0) n += (S.ends[0] >= b) + (S.ends[1] >= b);
+    return cta_count<NW>(S, n, flip);
+  };
+  const uint32_t kmin = KEY_MASKED + 1;  // the lowest finite logit
+  uint32_t lo = kmin, hi = key_of(top) + 1;  // groups at lo > most (once tested), at hi none
+  if (tid == 0) { S.n = 0; S.m = 0; }
+  bool crowded = false;
+  const bool many = floor > -INFINITY && unsigned(G) > most;
+  if (many) lo = max(lo, key_of(floor));  // every thread has a group there
+  if (many || groups_at(of_key(lo)) > most) {
+    for (int step = 0;; ++step) {
+      if (hi - lo <= 1) {
+        crowded = true;
+        break;
+      }
+      uint32_t mid = lo + (hi - lo) / 2;
+      if (step < 12) {
+        const float v = 0.5f * of_key(lo) + 0.5f * of_key(hi - 1);
+        mid = min(max(key_of(v), lo + 1), hi - 1);
+      }
+      const unsigned n = groups_at(of_key(mid));
+      if (n < K) hi = mid;
+      else if (n > most) lo = mid;
+      else { lo = mid; break; }
+    }
+  } else {
+    warps_sync<NW>();  // S.n, S.m
+  }
+  const float bound = of_key(lo);
+  unsigned n = 0;
+  if (!crowded) {
+    for (int k = 0; k < nst; ++k)
+      if (keys[k * G + tid] >= bound) S.list[atomicAdd(&S.m, 1u)] = unsigned(k * G + tid);
+    if (tid < 2 && S.ends[tid] >= bound) S.list[atomicAdd(&S.m, 1u)] = unsigned(nst * G + tid);
+    warps_sync<NW>();
+    const unsigned items = S.m * U;
+    auto push = [&](float v, unsigned idx) {
+      if (v >= bound) {
+        const unsigned at = atomicAdd(&S.n, 1u);
+        if (at < CAND) S.cand[at] = order_of(v, idx);
+      }
+    };
+    for (unsigned j = tid; j < items; j += G) {
+      const int g = int(S.list[j / U]), u = int(j % U);
+      if (g >= nst * G) {  // the ends
+        const int a = g == nst * G ? sl.lo : sl.tail0, b = g == nst * G ? sl.lo + sl.head : sl.hi;
+        for (int i = a + u; i < b; i += U) push(to_float(x[i]), unsigned(i));
+      } else {
+        const int v = g / G * SV + u * G + g % G;
+        if (v < sl.nv) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(body + int64_t(v) * E);
+          float2 f[E / 2];
+          Vec<T>::get(w, f);
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            push(f[i].x, unsigned(sl.lo + sl.head + v * E + 2 * i));
+            push(f[i].y, unsigned(sl.lo + sl.head + v * E + 2 * i + 1));
+          }
+        }
+      }
+    }
+    warps_sync<NW>();
+    n = S.n;
+  }
+  if (crowded || n > CAND) {
+    // the exact bound: the largest that K elements reach (elements of groups below it need not be read), then,
+    // among the elements equal to it, the index that leaves K
+    auto each = [&](float from, auto &&f) {
+      for (int k = 0; k < nst; ++k)
+        if (keys[k * G + tid] >= from)
+          for (int u = 0; u < U; ++u) {
+            const int v = k * SV + u * G + tid;
+            if (v < sl.nv)
+              for (int i = 0; i < E; ++i) f(to_float(body[int64_t(v) * E + i]), sl.lo + sl.head + v * E + i);
+          }
+      if (tid < 32) {
+        if (tid < sl.head) f(to_float(x[sl.lo + tid]), sl.lo + tid);
+        if (sl.tail0 + tid < sl.hi) f(to_float(x[sl.tail0 + tid]), sl.tail0 + tid);
+      }
+    };
+    auto elements_at = [&](float b) {
+      unsigned c = 0;
+      each(b, [&](float v, int) { c += v >= b; });
+      return cta_count<NW>(S, c, flip);
+    };
+    uint32_t l = lo, h = key_of(top) + 1;  // at least K reach l, none h
+    while (h - l > 1) {
+      const uint32_t mid = l + (h - l) / 2;
+      if (elements_at(of_key(mid)) >= K) l = mid;
+      else h = mid;
+    }
+    const float b = of_key(l);
+    unsigned c = 0;
+    each(b, [&](float v, int) { c += v > b; });
+    const unsigned left = K - cta_count<NW>(S, c, flip);
+    int il = sl.lo, ih = sl.hi;  // fewer than `left` equal ones before il, at least `left` before ih
+    while (ih - il > 1) {
+      const int mid = il + (ih - il) / 2;
+      c = 0;
+      each(b, [&](float v, int i) { c += v == b && i < mid; });
+      if (cta_count<NW>(S, c, flip) >= left) ih = mid;
+      else il = mid;
+    }
+    if (tid == 0) S.n = 0;
+    warps_sync<NW>();
+    each(b, [&](float v, int i) {
+      if (v > b || (v == b && i < ih)) {
+        const unsigned at = atomicAdd(&S.n, 1u);
+        if (at < CAND) S.cand[at] = order_of(v, unsigned(i));
+      }
+    });
+    warps_sync<NW>();
+    n = min(S.n, unsigned(CAND));
+  } else if (n > 2 * most) {
+    // many in the listed groups: a closer bound among the candidates (their order has no ties)
+    unsigned long long l = 0, h = ~0ull;
+    while (h - l > 1) {
+      const unsigned long long mid = l + (h - l) / 2;
+      unsigned c = 0;
+      for (unsigned i = tid; i < n; i += G) c += S.cand[i] >= mid;
+      c = cta_count<NW>(S, c, flip);
+      if (c < K) h = mid;
+      else if (c > most) l = mid;
+      else { l = mid; break; }
+    }
+    unsigned long long mine[CAND / G];
+#pragma unroll
+    for (int i = 0; i < CAND / G; ++i) {
+      const unsigned j = tid + i * G;
+      mine[i] = j < n && S.cand[j] >= l ? S.cand[j] : 0;
+    }
+    if (tid == 0) S.n = 0;
+    warps_sync<NW>();
+#pragma unroll
+    for (int i = 0; i < CAND / G; ++i)
+      if (mine[i]) S.cand[atomicAdd(&S.n, 1u)] = mine[i];
+    warps_sync<NW>();
+    n = S.n;
+  }
+  for (unsigned i = tid; i < K; i += G)
     if (i >= n) S.best[i] = 0;
-  for (unsigned i = threadIdx.x; i < n; i += NT) {
+  for (unsigned i = tid; i < n; i += G) {
     const unsigned long long mine = S.cand[i];
     unsigned above = 0;
+#pragma unroll 4
     for (unsigned j = 0; j < n; ++j) above += S.cand[j] > mine;
     if (above < K) S.best[above] = mine;
   }
-  __syncthreads();
+  warps_sync<NW>();
 }
 
 // ------------------------------------------------------------------ log probabilities
 
 struct LogpArgs {
   const void *x;
-  int64_t ld;
-  int V, K;
+  int64_t ld, T;
+  int V, K, stages;
   float scale;
   const int32_t *tokens;
   float *logp, *entropy, *top_logp, *saved;
@@ -195,249 +698,156 @@ struct LogpArgs {
   unsigned *errword;
 };
 
-// Shared memory of a row's slice when alternatives are wanted: the largest
-// logit of every chunk of CHUNK vectors (as ordered keys), chunk 0 being the
-// elements before the first vector and the last one those behind the last.
-constexpr int CHUNK = 4;
-template <typename T>
-__device__ __host__ inline int chunks_of(int nv) { return (nv + CHUNK - 1) / CHUNK + 2; }
-
-template <typename T, bool TOP, bool ENT>
-__global__ void __launch_bounds__(NT) logp_kernel(const LogpArgs a) {
-  constexpr int E = Slice<T>::E;
-  __shared__ float sm_m[NW], sm_s[NW], sm_t[NW];
-  __shared__ float part[3];
-  extern __shared__ __align__(16) unsigned char dyn[];
-  cg::cluster_group cl = cg::this_cluster();
-  const int size = int(cl.num_blocks()), rank = int(cl.block_rank());
-  const int64_t row = blockIdx.x / size;
-  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+// The computing warps' part.
+template <typename T, int NW, bool TOP, bool ENT>
+__device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, unsigned char *ring, int rank, int size,
+                                          int64_t first, int64_t step) {
+  constexpr int G = NW * 32, SV = G * U;
+  const int tid = threadIdx.x;
+  Select &S = *reinterpret_cast<Select *>(ring + a.stages * (SV * 16));
+  unsigned long long *gather = reinterpret_cast<unsigned long long *>(&S + 1);  // [size][K], the first CTA's
+  float *keys = reinterpret_cast<float *>(gather + (size > 1 ? size * a.K : 0));
   const float c = a.scale * LOG2E;
-  int token = -1;
-  bool skip = false;
-  if (a.tokens) {
-    token = a.tokens[row];
-    if (token >= a.V && threadIdx.x == 0 && rank == 0) atomicOr(a.errword, unsigned(ERR_BOUNDS));
-    skip = token < 0 || token >= a.V;
-  }
-  if (skip) {  // the whole cluster takes this way
-    if (rank != 0) return;
-    if (threadIdx.x == 0) {
-      if (a.logp) a.logp[row] = 0.f;
-      if (a.entropy) a.entropy[row] = 0.f;
-      if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int k = threadIdx.x; k < a.K; k += NT) {
-      a.top_tokens[row * a.K + k] = -1;
-      a.top_logp[row * a.K + k] = -INFINITY;
-    }
-    return;
-  }
-  const Slice<T> sl = slice_of(x, a.V, rank, size);
-  SelectSmem &S = *reinterpret_cast<SelectSmem *>(dyn);
-  uint32_t *keys = reinterpret_cast<uint32_t *>(dyn + (TOP ? sizeof(SelectSmem) : 0));
-  const int nchunks = chunks_of<T>(sl.nv);
-  Run r;
-  r.clear();
-  // the ragged ends: at most E - 1 elements each, one per thread of the first warp
-  if (threadIdx.x < 32) {
-    const int ih = sl.lo + int(threadIdx.x), it = sl.tail0 + int(threadIdx.x);
-    const bool ph = int(threadIdx.x) < sl.head, pt = it < sl.hi;
-    const float xh = ph ? to_float(x[ih]) : -INFINITY, xt = pt ? to_float(x[it]) : -INFINITY;
-    if (ph || pt) {
-      r.raise(fmaxf(xh, xt), c);
-      const float b = r.base();
-      if (ph) r.add<ENT>(xh, b, c);
-      if (pt) r.add<ENT>(xt, b, c);
-    }
-    if (TOP) {
-      const uint32_t kh = __reduce_max_sync(0xffffffffu, key_of(xh)), kt = __reduce_max_sync(0xffffffffu, key_of(xt));
-      if (threadIdx.x == 0) {
-        keys[0] = kh;
-        keys[nchunks - 1] = kt;
+  Spot at;
+  int par = 0, gathered = 0;
+  int token = a.tokens && first < a.T ? a.tokens[first] : -1;
+  for (int64_t row = first; row < a.T; row += step) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ld;
+    const int y = token;
+    if (a.tokens && row + step < a.T) token = a.tokens[row + step];
+    if (a.tokens && (y < 0 || y >= a.V)) {  // the whole cluster takes this way
+      if (rank != 0) continue;
+      if (tid == 0) {
+        if (y >= a.V) atomicOr(a.errword, unsigned(ERR_BOUNDS));
+        if (a.logp) a.logp[row] = 0.f;
+        if (a.entropy) a.entropy[row] = 0.f;
+        if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      if (TOP)
+        for (int k = tid; k < a.K; k += G) {
+          a.top_tokens[row * a.K + k] = -1;
+          a.top_logp[row * a.K + k] = -INFINITY;
+        }
+      continue;
     }
-  }
-  const T *body = x + sl.lo + sl.head;
-  constexpr int U = 4;
-  for (int i0 = 0; i0 < sl.nv; i0 += NT * U) {
-    RowVec<T, E> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NT + int(threadIdx.x);
-      if (i < sl.nv) v[u].load(body + int64_t(i) * E);
+    float xy = 0.f;
+    if (a.logp && rank == 0 && tid == 0) xy = to_float(x[y]);
+    const Slice<T> sl = slice_of(x, a.V, rank, size);
+    const int nst = (sl.nv + SV - 1) / SV;
+    Run r;
+    r.clear();
+    float xh = -INFINITY, xt = -INFINITY;
+    if (tid < 32) {
+      if (tid < sl.head) xh = to_float(x[sl.lo + tid]);
+      if (sl.tail0 + tid < sl.hi) xt = to_float(x[sl.tail0 + tid]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NT + int(threadIdx.x);
-      if (i0 + u * NT >= sl.nv) break;
-      float f[E];
-      float mx = -INFINITY;
-      if (i < sl.nv) {
-        v[u].get(f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) mx = fmaxf(mx, f[e]);
-        if (mx > r.m) r.raise(mx, c);
-        const float b = r.base();
-#pragma unroll
-        for (int e = 0; e < E; ++e) r.add<ENT>(f[e], b, c);
-      }
+    for (int k = 0; k < nst; ++k) {
+      uint4 v[U];
+      bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
+      read_stage<T, NW>(v, ring, at.st, sl.nv - k * SV);
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(&P.empty[at.st]);
+      at.next(a.stages);
+      const float mx = add_vectors<T, ENT>(r, v, c);
+      if (TOP) keys[k * G + tid] = mx;
+    }
+    float floor = r.m;
+    if (tid < 32) {
+      add_ends<T>(r, xh, xt, c);
       if (TOP) {
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if ((threadIdx.x & 3) == 0 && i < sl.nv) keys[1 + i / CHUNK] = key_of(mx);
-      }
-    }
-  }
-  // join: warp, CTA, cluster
-  r.join_warp(c);
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) { sm_m[warp] = r.m; sm_s[warp] = r.s; sm_t[warp] = r.t; }
-  __syncthreads();
-  Run all{sm_m[0], sm_s[0], sm_t[0]};
-#pragma unroll
-  for (int w = 1; w < NW; ++w) all.join(sm_m[w], sm_s[w], sm_t[w], c);
-  if (size > 1) {
-    if (threadIdx.x == 0) { part[0] = all.m; part[1] = all.s; part[2] = all.t; }
-    cl.sync();
-    all.clear();
-    for (int q = 0; q < size; ++q) {
-      const float *o = cl.map_shared_rank(part, q);
-      all.join(o[0], o[1], o[2], c);
-    }
-  }
-  const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
-  const float logs = logf(all.s);        // -inf for a row of masks
-  if (rank == 0 && threadIdx.x == 0) {
-    float H = 0.f;
-    if (bad) H = NAN;
-    else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
-    if (a.logp) {
-      const float xy = to_float(x[token]);
-      a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
-    }
-    if (a.entropy) a.entropy[row] = H;
-    if (a.saved)
-      reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
-  }
-  if (!TOP) {
-    if (size > 1) cl.sync();  // part is read by the others until here
-    return;
-  }
-  const unsigned K = unsigned(a.K);
-  if (bad) {
-    if (rank == 0)
-      for (unsigned k = threadIdx.x; k < K; k += NT) {
-        a.top_tokens[row * K + k] = -1;
-        a.top_logp[row * K + k] = NAN;
-      }
-    if (size > 1) cl.sync();
-    return;
-  }
-  // The K largest of the slice.  Elements are ordered by (logit, lower index
-  // first), chunks by (their largest logit, lower chunk first): each of the K
-  // best chunks holds an element that is above every element of a chunk behind
-  // them, so the K best elements lie in the K best chunks.
-  auto order = [](uint32_t key, uint32_t index) { return (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - index); };
-  const unsigned most = K + K / 2 < 32 ? 32 : K + K / 2;  // <= 192 <= 256
-  unsigned long long cb = 0;
-  if (unsigned(nchunks) > most)
-    cb = bound_for(K, most, ~0ull, &S.count, [&](unsigned long long b) {
-      unsigned n = 0;
-      for (int i = threadIdx.x; i < nchunks; i += NT) n += order(keys[i], i) >= b;
-      return n;
-    });
-  if (threadIdx.x == 0) { S.n = 0; S.m = 0; }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nchunks; i += NT)
-    if (keys[i] > KEY_MASKED && order(keys[i], i) >= cb) S.list[atomicAdd(&S.m, 1u)] = unsigned(i);
-  __syncthreads();
-  const unsigned nlist = S.m;
-  const uint32_t floor_key = max(uint32_t(cb >> 32), KEY_MASKED + 1);
-  // visit the elements of the listed chunks
-  auto visit = [&](auto &&f) {
-    for (unsigned j = threadIdx.x; j < nlist * (CHUNK * E); j += NT) {
-      const int ch = int(S.list[j / (CHUNK * E)]), w = int(j % (CHUNK * E));
-      int idx;
-      bool in;
-      if (ch == 0) { idx = sl.lo + w; in = w < sl.head; }
-      else if (ch == nchunks - 1) { idx = sl.tail0 + w; in = idx < sl.hi; }
-      else { idx = sl.lo + sl.head + (ch - 1) * (CHUNK * E) + w; in = idx < sl.tail0; }
-      if (in) f(key_of(to_float(x[idx])), unsigned(idx));
-    }
-  };
-  visit([&](uint32_t key, unsigned idx) {
-    if (key >= floor_key) {
-      const unsigned at = atomicAdd(&S.n, 1u);
-      if (at < CAND) S.cand[at] = order(key, idx);
-    }
-  });
-  __syncthreads();
-  unsigned n = S.n;
-  __syncthreads();
-  if (n > most) {
-    // too many at or above the chunks' bound (ties, or many large logits in few
-    // chunks): a closer bound, from the candidates or, if they did not all fit, the row
-    unsigned long long eb;
-    if (n <= CAND) {
-      eb = bound_for(K, most, ~0ull, &S.count, [&](unsigned long long b) {
-        unsigned k = 0;
-        for (unsigned i = threadIdx.x; i < n; i += NT) k += S.cand[i] >= b;
-        return k;
-      });
-    } else {
-      eb = bound_for(K, most, ~0ull, &S.count, [&](unsigned long long b) {
-        unsigned k = 0;
-        visit([&](uint32_t key, unsigned idx) { k += key >= floor_key && order(key, idx) >= b; });
-        return k;
-      });
-    }
-    if (threadIdx.x == 0) S.n = 0;
-    __syncthreads();
-    visit([&](uint32_t key, unsigned idx) {
-      if (key >= floor_key && order(key, idx) >= eb) S.cand[atomicAdd(&S.n, 1u)] = order(key, idx);
-    });
-    __syncthreads();
-    n = S.n;
-    __syncthreads();
-  }
-  rank_candidates(S, n, K);
-  if (size > 1) {
-    cl.sync();  // every slice's best is there (and `part` read)
-    if (rank == 0) {
-      // K from each slice: size * K <= CAND
-      for (unsigned i = threadIdx.x; i < size * K; i += NT) {
-        const unsigned long long *o = cl.map_shared_rank(S.best, i / K);
-        S.cand[i] = o[i % K];
-      }
-      __syncthreads();
-      // empty places (0) are equal to one another: rank only what is there
-      for (unsigned i = threadIdx.x; i < size * K; i += NT) {
-        const unsigned long long mine = S.cand[i];
-        unsigned above = 0;
-        for (unsigned j = 0; j < size * K; ++j) above += S.cand[j] > mine;
-        if (mine && above < K) {
-          a.top_tokens[row * K + above] = int32_t(0xffffffffu - uint32_t(mine));
-          a.top_logp[row * K + above] = (of_key(uint32_t(mine >> 32)) - all.m) * a.scale - logs;
+        const uint32_t kh = __reduce_max_sync(0xffffffffu, key_of(xh)), kt = __reduce_max_sync(0xffffffffu, key_of(xt));
+        if (tid == 0) {
+          S.ends[0] = of_key(kh);
+          S.ends[1] = of_key(kt);
         }
       }
-      // the places behind the last one found
-      unsigned have = 0;
-      for (unsigned i = threadIdx.x; i < size * K; i += NT) have += S.cand[i] != 0;
-      have = cta_sum(have, &S.count);
-      for (unsigned k = have + threadIdx.x; k < K; k += NT) {
-        a.top_tokens[row * K + k] = -1;
-        a.top_logp[row * K + k] = -INFINITY;
-      }
     }
-    cl.sync();  // S.best is read by the first CTA until here
-    return;
+    const Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, TOP ? &floor : nullptr, !TOP && size == 1);
+    par ^= 1;
+    if (!TOP && size == 1 && tid >= 32) continue;
+    const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
+    const float logs = logf(all.s);        // -inf for a row of masks
+    if (rank == 0 && tid == 0) {
+      float H = 0.f;
+      if (bad) H = NAN;
+      else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
+      if (a.logp) a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
+      if (a.entropy) a.entropy[row] = H;
+      if (a.saved)
+        reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
+    }
+    if (!TOP) continue;
+    const unsigned K = unsigned(a.K);
+    if (bad) {
+      if (rank == 0)
+        for (unsigned k = tid; k < K; k += G) {
+          a.top_tokens[row * K + k] = -1;
+          a.top_logp[row * K + k] = NAN;
+        }
+      continue;
+    }
+    auto put = [&](unsigned k, unsigned long long b) {
+      a.top_tokens[row * K + k] = b ? int32_t(0xffffffffu - uint32_t(b)) : -1;
+      a.top_logp[row * K + k] = b ? (of_key(uint32_t(b >> 32)) - all.m) * a.scale - logs : -INFINITY;
+    };
+    select_largest<T, NW>(S, keys, x, sl, nst, K, floor, all.m);
+    if (size == 1) {
+      for (unsigned k = tid; k < K; k += G) put(k, S.best[k]);
+      warps_sync<NW>();  // S is written again in the next row
+      continue;
+    }
+    // the CTAs' lists to the first one, which merges them: an element's place is its place in its list plus the
+    // numbers of larger elements in the others
+    for (unsigned k = tid; k < K; k += G)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_at(smem_at(gather + rank * K + k), 0)), "l"(S.best[k])
+                   : "memory");
+    warps_sync<NW>();
+    if (tid == 0) bar_arrive_peer(&P.gather, 0);
+    if (rank != 0) continue;
+    bar_wait(&P.gather, gathered, &P.abort, a.errword);
+    gathered ^= 1;
+    unsigned found = 0;
+    for (unsigned i = tid; i < size * K; i += G) {
+      const unsigned long long mine = gather[i];
+      if (!mine) continue;
+      ++found;
+      unsigned place = i % K;
+      for (int q = 0; q < size; ++q) {
+        if (q == int(i / K)) continue;
+        unsigned l = 0, h = K;  // the first place of list q that is not larger
+        while (l < h) {
+          const unsigned mid = (l + h) / 2;
+          if (gather[q * K + mid] > mine) l = mid + 1;
+          else h = mid;
+        }
+        place += l;
+      }
+      if (place < K) put(place, mine);
+    }
+    int flip = 0;
+    found = cta_count<NW>(S, found, flip);
+    for (unsigned k = found + tid; k < K; k += G) put(k, 0);
+    warps_sync<NW>();
   }
-  for (unsigned k = threadIdx.x; k < K; k += NT) {
-    const unsigned long long b = S.best[k];
-    a.top_tokens[row * K + k] = b ? int32_t(0xffffffffu - uint32_t(b)) : -1;
-    a.top_logp[row * K + k] = b ? (of_key(uint32_t(b >> 32)) - all.m) * a.scale - logs : -INFINITY;
-  }
+}
+
+// NW warps compute, one more streams the rows.
+template <typename T, int NW, bool TOP, bool ENT>
+__global__ void __launch_bounds__((NW + 1) * 32, per_sm<NW>(!TOP)) logp_kernel(const LogpArgs a) {
+  __shared__ Pipe P;
+  extern __shared__ __align__(128) unsigned char ring[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int size = int(cl.num_blocks()), rank = int(cl.block_rank());
+  const int64_t first = blockIdx.x / size, step = gridDim.x / size;
+  pipe_init<NW>(P, a.stages, size, cl);
+  if (threadIdx.x >= NW * 32)
+    produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, false, a.errword, [&](int64_t row) {
+      const int t = a.tokens ? a.tokens[row] : 0;
+      return t >= 0 && t < a.V;
+    });
+  else
+    logp_rows<T, NW, TOP, ENT>(a, P, ring, rank, size, first, step);
+  if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
 // ------------------------------------------------------------------ writing a gradient row
@@ -481,16 +891,16 @@ __device__ __forceinline__ void map_slice(const T *x, T *out, const Slice<T> &sl
   }
 }
 
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void zero_slice(T *out, int lo, int hi) {
   constexpr int E = Slice<T>::E;
   int head = int(((16 - (reinterpret_cast<uintptr_t>(out + lo) & 15)) & 15) / sizeof(T));
   if (head > hi - lo) head = hi - lo;
   if (int(threadIdx.x) < head) out[lo + threadIdx.x] = from_float<T>(0.f);
   const int nv = (hi - lo - head) / E;
-  for (int i = threadIdx.x; i < nv; i += NT)
+  for (int i = threadIdx.x; i < nv; i += N)
     *reinterpret_cast<uint4 *>(out + lo + head + int64_t(i) * E) = make_uint4(0u, 0u, 0u, 0u);
-  for (int i = lo + head + nv * E + int(threadIdx.x); i < hi; i += NT) out[i] = from_float<T>(0.f);
+  for (int i = lo + head + nv * E + int(threadIdx.x); i < hi; i += N) out[i] = from_float<T>(0.f);
 }
 
 struct LogpGradArgs {
@@ -522,7 +932,7 @@ __global__ void __launch_bounds__(NT) logp_grad_kernel(const LogpGradArgs a) {
   }
   const float4 sv = reinterpret_cast<const float4 *>(a.saved)[row];
   if (skip || sv.x == -INFINITY) {
-    zero_slice(out, sl.lo, sl.hi);
+    zero_slice<T, NT>(out, sl.lo, sl.hi);
     return;
   }
   const float c = a.scale * LOG2E, L = sv.y * LOG2E;
@@ -557,8 +967,8 @@ __global__ void __launch_bounds__(NT) logp_grad_kernel(const LogpGradArgs a) {
 struct DistillArgs {
   const void *x;
   void *out;
-  int64_t ld, ldd;
-  int V, K, tail, parts;
+  int64_t ld, ldd, T;
+  int V, K, tail, parts, stages;
   float scale, value_scale;
   const int32_t *tokens;
   const float *values, *dloss;
@@ -569,98 +979,137 @@ struct DistillArgs {
 // A row's teacher entries in shared memory.
 struct Teacher {
   float q[MAX_K], lq[MAX_K], x[MAX_K];
+  float sum[MAX_K];  // of a token's first entry: the q of all its entries
   int idx[MAX_K];    // -1: left out
   int first[MAX_K];  // whether no earlier entry has the same token
   float rest;        // q_r
   float m, s;        // running sum of the student's logits at the distinct tokens
   int live;          // entries that count
   int distinct;      // tokens among them
+  // tail: the slice's vectors that the marks are of, and the marks of its ends
+  int base, nv;
+  unsigned head, behind;
 };
 
 // Loads the entries, their probabilities q and ln q, and the student's logits
-// at those in [lo, hi).  All NT threads; returns after a barrier.
+// at those in [lo, hi).  One warp.
 template <typename T>
 __device__ void load_teacher(Teacher &S, const DistillArgs &a, int64_t row, const T *x, int lo, int hi, bool report) {
-  const int k = threadIdx.x;
-  if (k < a.K) {
-    int t = a.tokens[row * a.K + k];
-    if (t >= a.V && report) atomicOr(a.errword, unsigned(ERR_BOUNDS));
-    if (t >= a.V || t < 0) t = -1;
-    S.idx[k] = t;
-    S.lq[k] = t < 0 ? -INFINITY : a.values[row * a.K + k] * a.value_scale;
-    S.x[k] = t >= lo && t < hi ? to_float(x[t]) : -INFINITY;
-  }
-  __syncthreads();
-  if (k < a.K) {
-    bool first = true;
-    for (int j = 0; j < k; ++j) first = first && S.idx[j] != S.idx[k];
-    S.first[k] = first && S.idx[k] >= 0;
-  }
-  if (threadIdx.x < 32) {
-    // the sums of up to four entries per lane
-    float mx = -INFINITY;
-    int n = 0;
-    for (int j = threadIdx.x; j < a.K; j += 32) {
-      mx = fmaxf(mx, S.lq[j]);
-      n += S.idx[j] >= 0;
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
+  constexpr int Q = MAX_K / 32;  // entries of a lane
+  const int lane = threadIdx.x & 31;
+  const float c = a.scale * LOG2E;
+  int t[Q];
+  float lq[Q], xs[Q], q[Q];
+  float mx = -INFINITY;
+  int n = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (a.tail || mx == -INFINITY) mx = 0.f;
-    float s = 0.f;
-    for (int j = threadIdx.x; j < a.K; j += 32) s += S.idx[j] >= 0 ? expf(S.lq[j] - mx) : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (!a.tail && s == 0.f) n = 0;  // nothing but -inf: no teacher
-    const float ls = a.tail ? 0.f : mx + logf(s);
-    for (int j = threadIdx.x; j < a.K; j += 32) {
-      const float l = S.lq[j] - ls;
-      S.lq[j] = l;
-      S.q[j] = S.idx[j] >= 0 && n ? (a.tail ? expf(l) : expf(l + ls - mx) / s) : 0.f;
-    }
-    if (threadIdx.x == 0) {
-      S.live = n;
-      const float rest = 1.f - s;
-      S.rest = a.tail && !(rest < float(n) * 1.1920929e-7f) ? rest : 0.f;
+  for (int i = 0; i < Q; ++i) {
+    const int k = lane + 32 * i;
+    t[i] = -1;
+    lq[i] = xs[i] = -INFINITY;
+    if (k < a.K) {
+      t[i] = a.tokens[row * a.K + k];
+      lq[i] = a.values[row * a.K + k] * a.value_scale;
     }
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    Run r;
-    r.clear();
-    int n = 0;
-    const float c = a.scale * LOG2E;
-    for (int j = threadIdx.x; j < a.K; j += 32)
-      if (S.first[j]) {
-        r.raise(fmaxf(r.m, S.x[j]), c);
-        r.add<false>(S.x[j], r.base(), c);
-        ++n;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    if (t[i] >= a.V && report) atomicOr(a.errword, unsigned(ERR_BOUNDS));
+    if (t[i] < 0 || t[i] >= a.V) {
+      t[i] = -1;
+      lq[i] = -INFINITY;
+    }
+    if (t[i] >= lo && t[i] < hi) xs[i] = to_float(x[t[i]]);
+    if (lane + 32 * i < a.K) S.idx[lane + 32 * i] = t[i];
+    mx = fmaxf(mx, lq[i]);
+    n += t[i] >= 0;
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (a.tail || mx == -INFINITY) mx = 0.f;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    q[i] = t[i] >= 0 ? expf(lq[i] - mx) : 0.f;
+    s += q[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (!a.tail && s == 0.f) n = 0;  // nothing but -inf: no teacher
+  const float ls = a.tail ? 0.f : mx + logf(s);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int k = lane + 32 * i;
+    lq[i] -= ls;
+    if (!a.tail) q[i] = n ? q[i] / s : 0.f;
+    if (k < a.K) {
+      S.q[k] = q[i];
+      S.lq[k] = lq[i];
+      S.x[k] = xs[i];
+    }
+  }
+  __syncwarp();
+  // a token's first entry, and the sum over all its entries
+  float sum[Q];
+  bool first[Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    sum[i] = 0.f;
+    first[i] = t[i] >= 0;
+  }
+  for (int j = 0; j < a.K; ++j) {
+    const int tj = S.idx[j];
+    const float qj = S.q[j];
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      if (tj == t[i]) {
+        first[i] = first[i] && j >= lane + 32 * i;
+        sum[i] += qj;
       }
-    r.t = 0.f;
-    r.join_warp(c);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (threadIdx.x == 0) {
-      S.m = r.m;
-      S.s = r.s;
-      S.distinct = n;
+  }
+  float m = -INFINITY, es = 0.f;
+  int distinct = 0;
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+    if (first[i]) {
+      m = fmaxf(m, xs[i]);
+      ++distinct;
+    }
+  m = of_key(__reduce_max_sync(0xffffffffu, key_of(m)));
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int k = lane + 32 * i;
+    if (first[i]) es += ex2((xs[i] - (m == -INFINITY ? 0.f : m)) * c);
+    if (k < a.K) {
+      S.first[k] = first[i];
+      S.sum[k] = sum[i];
     }
   }
-  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
+  distinct = __reduce_add_sync(0xffffffffu, distinct);
+  if (lane == 0) {
+    S.live = n;
+    const float rest = 1.f - s;
+    S.rest = a.tail && !(rest < float(n) * 1.1920929e-7f) ? rest : 0.f;
+    S.m = m;
+    S.s = es;
+    S.distinct = distinct;
+  }
+  __syncwarp();
 }
 
 // Puts the teacher's tokens of the slice [lo, hi) right after the other
-// elements were written: (p - q) g.
+// elements were written: (p - q) g.  All threads of the CTA that compute.
 template <typename T>
 __device__ __forceinline__ void write_teacher(const Teacher &S, const DistillArgs &a, T *out, int lo, int hi, float M,
-                                              float logs, float g) {
-  const int k = threadIdx.x;
-  if (k < a.K && S.first[k] && S.idx[k] >= lo && S.idx[k] < hi) {
-    float q = 0.f;
-    for (int j = k; j < a.K; ++j) q += S.idx[j] == S.idx[k] ? S.q[j] : 0.f;
-    const float p = S.x[k] == -INFINITY ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
-    out[S.idx[k]] = from_float<T>((p - q) * g);
-  }
+                                              float logs, float g, int threads) {
+  for (int k = threadIdx.x; k < a.K; k += threads)
+    if (S.first[k] && S.idx[k] >= lo && S.idx[k] < hi) {
+      const float p = S.x[k] == -INFINITY ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
+      out[S.idx[k]] = from_float<T>((p - S.sum[k]) * g);
+    }
 }
 
 // The gradient of the tokens outside the teacher's: f exp(scale (x - M) - L).
@@ -680,149 +1129,231 @@ __device__ __forceinline__ Outside outside_of(const Teacher &S, int tail, float 
   return o;
 }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a) {
-  constexpr int E = Slice<T>::E;
-  __shared__ Teacher S;
-  __shared__ float sm_m[NW], sm_s[NW];
-  __shared__ float part[2];
-  extern __shared__ __align__(16) unsigned bits[];  // tail: one bit per element of the slice, a vector's E bits side by side
-  cg::cluster_group cl = cg::this_cluster();
-  const int size = int(cl.num_blocks()), rank = int(cl.block_rank());
-  const int64_t row = blockIdx.x / size;
-  const T *x = static_cast<const T *>(a.x) + row * a.ld;
-  const Slice<T> sl = slice_of(x, a.V, rank, size);
+// Whether a row has a teacher (the same decision as load_teacher's live), by one warp.
+__device__ __forceinline__ bool has_teacher(const DistillArgs &a, int64_t row) {
+  bool any = false;
+  for (int k = threadIdx.x & 31; k < a.K; k += 32) {
+    const int t = a.tokens[row * a.K + k];
+    const float v = a.values[row * a.K + k] * a.value_scale;
+    any = any || (t >= 0 && t < a.V && (a.tail || v != -INFINITY));
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
+// The marks of a slice's vectors, a byte each.
+template <typename T>
+__host__ __device__ inline int mark_bytes_of(int V, int size) { return (V / Vec<T>::E / size + 2 + 15) / 16 * 16; }
+
+// One warp's part: the teacher's entries of the rows to come.
+template <typename T>
+__device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teacher (&teachers)[2], unsigned char *marks,
+                                             int mark_bytes, int rank, int size, int64_t first, int64_t step) {
+  constexpr int E = Vec<T>::E;
+  int64_t n = 0;
+  for (int64_t row = first; row < a.T; row += step, ++n) {
+    Teacher &S = teachers[n & 1];
+    bar_wait(&P.tempty[n & 1], uint32_t(n >> 1 & 1) ^ 1, &P.abort, a.errword);
+    const T *x = static_cast<const T *>(a.x) + row * a.ld;
+    unsigned *words = reinterpret_cast<unsigned *>(marks + (n & 1) * mark_bytes);
+    const int lane = threadIdx.x & 31;
+    if (a.tail)  // the marks of the buffer's last row
+      for (int k = lane; k < a.K; k += 32) {
+        const int i = S.idx[k] - S.base;
+        if (S.nv && S.idx[k] >= 0 && i >= 0 && i < S.nv * E) words[i / E / 4] = 0u;
+      }
+    __syncwarp();
+    load_teacher(S, a, row, x, 0, a.V, rank == 0);
+    if (a.tail) {
+      const Slice<T> sl = slice_of(x, a.V, rank, size);
+      const int base = sl.lo + sl.head;
+      unsigned head = 0, behind = 0;
+      for (int k = lane; k < a.K; k += 32) {
+        const int t = S.idx[k], i = t - base;
+        if (t < 0) continue;
+        if (i >= 0 && i < sl.nv * E) atomicOr(&words[i / E / 4], 1u << (i / E % 4 * 8 + i % E));
+        else if (t >= sl.lo && t < base) head |= 1u << (t - sl.lo);
+        else if (t >= sl.tail0 && t < sl.hi) behind |= 1u << (t - sl.tail0);
+      }
+      __syncwarp();
+      head = __reduce_or_sync(0xffffffffu, head);
+      behind = __reduce_or_sync(0xffffffffu, behind);
+      if (lane == 0) {
+        S.base = base;
+        S.nv = sl.nv;
+        S.head = head;
+        S.behind = behind;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(&P.tfull[n & 1]);
+  }
+}
+
+// The computing warps' part.
+template <typename T, int NW, bool GRAD>
+__device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, const Teacher (&teachers)[2],
+                                             const unsigned char *ring, const unsigned char *marks, int mark_bytes,
+                                             int rank, int size, int64_t first, int64_t step) {
+  constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E;
+  const int tid = threadIdx.x;
   const float c = a.scale * LOG2E;
-  load_teacher(S, a, row, x, 0, a.V, rank == 0);
-  T *out = GRAD ? static_cast<T *>(a.out) + row * a.ldd : nullptr;
-  if (S.live == 0) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.loss[row] = 0.f;
-      if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+  Spot at;
+  int par = 0;
+  int64_t n = 0;
+  for (int64_t row = first; row < a.T; row += step, ++n) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ld;
+    const Slice<T> sl = slice_of(x, a.V, rank, size);
+    T *out = GRAD ? static_cast<T *>(a.out) + row * a.ldd : nullptr;
+    const Teacher &S = teachers[n & 1];
+    bar_wait(&P.tfull[n & 1], uint32_t(n >> 1 & 1), &P.abort, a.errword);
+    auto release = [&]() {
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(&P.tempty[n & 1]);
+    };
+    if (S.live == 0) {
+      if (rank == 0 && tid == 0) {
+        a.loss[row] = 0.f;
+        if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (GRAD) zero_slice<T, G>(out, sl.lo, sl.hi);
+      release();
+      continue;
+    }
+    const int nst = (sl.nv + SV - 1) / SV;
+    const bool stays = GRAD && nst <= a.stages;
+    const unsigned char *mark = marks + (n & 1) * mark_bytes;
+    Run r;
+    r.clear();
+    float xh = -INFINITY, xt = -INFINITY;
+    if (tid < 32) {
+      if (tid < sl.head) xh = to_float(x[sl.lo + tid]);
+      if (sl.tail0 + tid < sl.hi) xt = to_float(x[sl.tail0 + tid]);
+      const bool mh = a.tail && (S.head >> tid & 1u), mt = a.tail && (S.behind >> tid & 1u);
+      add_ends<T>(r, mh ? -INFINITY : xh, mt ? -INFINITY : xt, c);
+    }
+    Spot again = at;
+    for (int k = 0; k < nst; ++k) {
+      uint4 v[U];
+      bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
+      read_stage<T, NW>(v, ring, at.st, sl.nv - k * SV);
+      if (!stays) {
+        __syncwarp();
+        if ((tid & 31) == 0) bar_arrive(&P.empty[at.st]);
+      }
+      at.next(a.stages);
+      if (a.tail) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = k * SV + u * G + tid;
+          const unsigned b = i < sl.nv ? mark[i] : 0u;
+          if (b) Vec<T>::mask(v[u], b);
+        }
+      }
+      add_vectors<T, false>(r, v, c);
+    }
+    Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, nullptr);
+    par ^= 1;
+    // tail: `all` is the sum over the tokens outside the teacher's; add the teacher's
+    float ltail = 0.f;
+    if (a.tail) {
+      const Sums o = all;
+      all.m = fmaxf(o.m, S.m);
+      all.s = o.s * ex2((o.m - all.base()) * c) + S.s * ex2((S.m - all.base()) * c);
+      ltail = o.s == 0.f ? -INFINITY : (o.m - all.base()) * a.scale + logf(o.s);
+    }
+    const bool bad = !(all.s < INFINITY);
+    const bool empty = all.s == 0.f;
+    const float logs = logf(all.s);
+    const float M = all.m;
+    if (rank == 0 && tid < 32) {
+      float l = 0.f;
+      for (int k = tid; k < a.K; k += 32)
+        if (S.idx[k] >= 0 && S.q[k] != 0.f)
+          l += S.q[k] * (S.lq[k] - (empty || S.x[k] == -INFINITY ? -INFINITY : (S.x[k] - M) * a.scale - logs));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (tid == 0) {
+        if (a.tail && S.rest > 0.f && S.distinct < a.V)
+          l += S.rest * (logf(S.rest) - (empty ? -INFINITY : ltail - logs));
+        a.loss[row] = bad ? NAN : l;
+        if (a.saved)
+          reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : M, bad ? NAN : logs, 0.f, bad ? NAN : ltail);
+      }
     }
     if (GRAD) {
-      if (size > 1) cl.sync();  // out may be x: the entries' logits have been read
-      zero_slice(out, sl.lo, sl.hi);
-    }
-    return;
-  }
-  // mark the teacher's tokens of this slice: element sl.lo + sl.head + i at bit E + i,
-  // the elements before the first vector below, those behind the last above
-  const int base = sl.lo + sl.head - E;
-  if (a.tail) {
-    const int words = ((sl.nv + 2) * E + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += NT) bits[i] = 0u;
-    __syncthreads();
-    const int k = threadIdx.x;
-    if (k < a.K && S.idx[k] >= sl.lo && S.idx[k] < sl.hi)
-      atomicOr(&bits[(S.idx[k] - base) >> 5], 1u << ((S.idx[k] - base) & 31));
-    __syncthreads();
-  }
-  auto marked = [&](int idx) { return a.tail && ((bits[(idx - base) >> 5] >> ((idx - base) & 31)) & 1u); };
-  Run r;
-  r.clear();
-  if (threadIdx.x < 32) {
-    const int ih = sl.lo + int(threadIdx.x), it = sl.tail0 + int(threadIdx.x);
-    const bool ph = int(threadIdx.x) < sl.head, pt = it < sl.hi;
-    const float xh = ph && !marked(ih) ? to_float(x[ih]) : -INFINITY;
-    const float xt = pt && !marked(it) ? to_float(x[it]) : -INFINITY;
-    if (ph || pt) {
-      r.raise(fmaxf(xh, xt), c);
-      const float b = r.base();
-      r.add<false>(xh, b, c);
-      r.add<false>(xt, b, c);
-    }
-  }
-  const T *body = x + sl.lo + sl.head;
-  constexpr int U = 4;
-  for (int i0 = 0; i0 < sl.nv; i0 += NT * U) {
-    RowVec<T, E> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NT + int(threadIdx.x);
-      if (i < sl.nv) v[u].load(body + int64_t(i) * E);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NT + int(threadIdx.x);
-      if (i >= sl.nv) break;
-      float f[E];
-      v[u].get(f);
-      if (a.tail) {
-        const unsigned mk = (bits[((i + 1) * E) >> 5] >> (((i + 1) * E) & 31)) & ((1u << E) - 1u);
-        if (mk)
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if ((mk >> e) & 1u) f[e] = -INFINITY;
+      const float g = (a.dloss ? a.dloss[row] : 1.f) * a.scale;
+      Outside o = outside_of(S, a.tail, logs, ltail);
+      if (bad) o.f = NAN;
+      // a row of masks: 0 everywhere
+      const float A = empty ? 0.f : o.f * g, L = empty ? 0.f : o.L * LOG2E, base = empty ? 0.f : M;
+      const float2 A2 = both(A), nL = both(-L), nM = both(-base), c2 = both(c);
+      auto grad = [&](float v) { return A * ex2(fmaf(v - base, c, -L)); };
+      T *to = out + sl.lo + sl.head;
+      const bool aligned = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
+      if (tid < 32) {
+        if (tid < sl.head) out[sl.lo + tid] = from_float<T>(grad(xh));
+        if (sl.tail0 + tid < sl.hi) out[sl.tail0 + tid] = from_float<T>(grad(xt));
       }
-      float mx = -INFINITY;
+      Spot &from = stays ? again : at;
+      for (int k = 0; k < nst; ++k) {
+        uint4 v[U];
+        if (!stays) bar_wait(&P.full[from.st], from.ph, &P.abort, a.errword);
+        read_stage<T, NW>(v, ring, from.st, sl.nv - k * SV);
+        __syncwarp();
+        if ((tid & 31) == 0) bar_arrive(&P.empty[from.st]);
+        from.next(a.stages);
 #pragma unroll
-      for (int e = 0; e < E; ++e) mx = fmaxf(mx, f[e]);
-      if (mx > r.m) r.raise(mx, c);
-      const float b = r.base();
+        for (int u = 0; u < U; ++u) {
+          const int i = k * SV + u * G + tid;
+          if (i >= sl.nv) break;
+          float2 f[E / 2];
+          Vec<T>::get(v[u], f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) r.add<false>(f[e], b, c);
+          for (int e = 0; e < E / 2; ++e) f[e] = mul2(ex2(fma2(add2(f[e], nM), c2, nL)), A2);
+          if (aligned) {
+            *reinterpret_cast<uint4 *>(to + int64_t(i) * E) = Vec<T>::put(f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) to[int64_t(i) * E + e] = from_float<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
+          }
+        }
+      }
+      warps_sync<NW>();
+      if (!empty) write_teacher(S, a, out, sl.lo, sl.hi, bad ? NAN : M, logs, g, G);
     }
+    release();
   }
-  r.t = 0.f;
-  r.join_warp(c);
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) { sm_m[warp] = r.m; sm_s[warp] = r.s; }
-  __syncthreads();
-  Run all{sm_m[0], sm_s[0], 0.f};
-#pragma unroll
-  for (int w = 1; w < NW; ++w) all.join(sm_m[w], sm_s[w], 0.f, c);
-  if (size > 1) {
-    if (threadIdx.x == 0) { part[0] = all.m; part[1] = all.s; }
-    cl.sync();
-    all.clear();
-    for (int q = 0; q < size; ++q) {
-      const float *o = cl.map_shared_rank(part, q);
-      all.join(o[0], o[1], 0.f, c);
-    }
-    cl.sync();  // everything of the row that the first pass reads has been read
-  } else {
-    __syncthreads();
-  }
-  // tail: `all` is the sum over the tokens outside the teacher's; add the teacher's
-  float ltail = 0.f;
-  if (a.tail) {
-    const Run others = all;
-    all.join(S.m, S.s, 0.f, c);
-    ltail = others.s == 0.f ? -INFINITY : (others.m - all.base()) * a.scale + logf(others.s);
-  }
-  const bool bad = !(all.s < INFINITY);
-  const bool empty = all.s == 0.f;
-  const float logs = logf(all.s);
-  const float M = all.m;
-  if (rank == 0 && threadIdx.x < 32) {
-    float l = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += 32)
-      if (S.idx[k] >= 0 && S.q[k] != 0.f)
-        l += S.q[k] * (S.lq[k] - (empty || S.x[k] == -INFINITY ? -INFINITY : (S.x[k] - M) * a.scale - logs));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (threadIdx.x == 0) {
-      if (a.tail && S.rest > 0.f && S.distinct < a.V)
-        l += S.rest * (logf(S.rest) - (empty ? -INFINITY : ltail - logs));
-      a.loss[row] = bad ? NAN : l;
-      if (a.saved)
-        reinterpret_cast<float4 *>(a.saved)[row] =
-            make_float4(bad ? NAN : M, bad ? NAN : logs, 0.f, bad ? NAN : ltail);
-    }
-  }
-  if (!GRAD) return;
-  if (empty) {
-    zero_slice(out, sl.lo, sl.hi);
-    return;
-  }
-  const float g = (a.dloss ? a.dloss[row] : 1.f) * a.scale;
-  Outside o = outside_of(S, a.tail, logs, ltail);
-  if (bad) o.f = NAN;
-  const float A = o.f * g, L = o.L * LOG2E;
-  map_slice(x, out, sl, [=](int, float v) { return A * ex2(fmaf(v - M, c, -L)); });
-  __syncthreads();
-  write_teacher(S, a, out, sl.lo, sl.hi, bad ? NAN : M, logs, g);
+}
+
+// NW warps compute, one streams the rows, one loads the teacher's entries of
+// the rows to come.  With the tail as one more outcome the sum runs over the
+// tokens outside the teacher's alone (they may be all that is left of 1 in
+// float), so the teacher's are marked, a bit each, and masked as they are read.
+// A row whose slice fits the ring stays there for its gradient; a longer one is
+// streamed a second time (from L2).
+template <typename T, int NW, bool GRAD>
+__global__ void __launch_bounds__((NW + 2) * 32, per_sm<NW>(false)) distill_kernel(const DistillArgs a) {
+  constexpr int G = NW * 32;
+  __shared__ Pipe P;
+  __shared__ Teacher teachers[2];
+  extern __shared__ __align__(128) unsigned char ring[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int size = int(cl.num_blocks()), rank = int(cl.block_rank());
+  const int64_t first = blockIdx.x / size, step = gridDim.x / size;
+  const int tid = threadIdx.x;
+  const int mark_bytes = a.tail ? mark_bytes_of<T>(a.V, size) : 0;
+  unsigned char *marks = ring + a.stages * (G * U * 16);
+  for (int i = tid; i < 2 * mark_bytes / 4; i += (NW + 2) * 32) reinterpret_cast<unsigned *>(marks)[i] = 0u;
+  if (tid < 2) teachers[tid].nv = 0;
+  pipe_init<NW>(P, a.stages, size, cl);
+  if (tid >= G + 32)
+    teacher_rows<T>(a, P, teachers, marks, mark_bytes, rank, size, first, step);
+  else if (tid >= G)
+    produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, GRAD, a.errword,
+                   [&](int64_t row) { return has_teacher(a, row); });
+  else
+    distill_rows<T, NW, GRAD>(a, P, teachers, ring, marks, mark_bytes, rank, size, first, step);
+  if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
 template <typename T>
@@ -834,10 +1365,11 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
   T *out = static_cast<T *>(a.out) + row * a.ldd;
   const Slice<T> sl = slice_of(x, a.V, part, a.parts);
   // only this part's logits: in place, the other parts may already be gradients
-  load_teacher(S, a, row, x, sl.lo, sl.hi, part == 0);
+  if (threadIdx.x < 32) load_teacher(S, a, row, x, sl.lo, sl.hi, part == 0);
+  __syncthreads();
   const float4 sv = reinterpret_cast<const float4 *>(a.saved)[row];
   if (S.live == 0 || sv.x == -INFINITY) {
-    zero_slice(out, sl.lo, sl.hi);
+    zero_slice<T, NT>(out, sl.lo, sl.hi);
     return;
   }
   const float c = a.scale * LOG2E;
@@ -846,7 +1378,7 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
   const float A = o.f * g, L = o.L * LOG2E, M = sv.x;
   map_slice(x, out, sl, [=](int, float v) { return A * ex2(fmaf(v - M, c, -L)); });
   __syncthreads();
-  write_teacher(S, a, out, sl.lo, sl.hi, M, sv.y, g);
+  write_teacher(S, a, out, sl.lo, sl.hi, M, sv.y, g, NT);
 }
 
 // ------------------------------------------------------------------ launch shapes and checks
@@ -888,46 +1420,87 @@ poet_status check_out(const char *what, const void *x, int64_t ld, const void *o
 }
 bool al(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <typename K, typename A>
-poet_status launch_rows(K kern, const A &a, int64_t T, int cluster, size_t smem, cudaStream_t st, const char *what) {
-  if (smem > 32 * 1024) POET_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+// How the rows are spread: CTAs of NW computing warps, clusters of `cluster` of
+// them, and the stages that fit beside `extra` bytes where `per_sm` CTAs share an SM.
+struct Spread {
+  int cluster, stages;
+  unsigned grid;
+  size_t smem;
+};
+template <int NW>
+Spread spread(int64_t rows, int cluster, size_t extra, int per_sm) {
+  constexpr size_t STAGE = size_t(NW) * 32 * U * 16, STATIC = 10 * 1024, SM = 228 * 1024;
+  Spread s;
+  s.cluster = cluster;
+  size_t left = 0;
+  for (;; --per_sm) {  // at least four stages, or two of one CTA alone
+    left = std::min<size_t>(SM / per_sm - STATIC, 227 * 1024 - STATIC);
+    if (left >= extra + 4 * STAGE || per_sm == 1) break;
+  }
+  s.stages = int(std::min<size_t>((left - extra) / STAGE, MAX_STAGES));
+  s.smem = s.stages * STAGE + extra;
+  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(num_sms()) * per_sm / cluster)) * cluster);
+  return s;
+}
+
+template <auto KERN, typename A>
+poet_status launch_rows(const A &a, const Spread &s, int threads, cudaStream_t st, const char *what) {
+  POET_TRY(allow_smem<KERN>(s.smem));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.x = unsigned(s.cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(T * cluster));
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(s.grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = s.smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  POET_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a));
+  POET_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERN, a));
   count_launch();
   return launch_status(what);
 }
 
-template <typename T>
-poet_status run_logp(const LogpArgs &a, int64_t rows, cudaStream_t st) {
-  const int cluster = cluster_of(rows, a.V);
-  const int nv = a.V / Slice<T>::E / cluster + 1;
-  const size_t smem = a.K ? sizeof(SelectSmem) + size_t(chunks_of<T>(nv)) * 4 : 0;
+// Columns up to which two warps work on a row and not eight.
+constexpr int NARROW = 8192;
+
+template <typename T, int NW>
+poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
+  constexpr int THREADS = (NW + 1) * 32;
+  const int64_t nv = a.V / Vec<T>::E / cluster + 1, nst = (nv + NW * 32 * U - 1) / (NW * 32 * U);
+  size_t extra = 0;
+  if (a.K)
+    extra = sizeof(Select) + (cluster > 1 ? size_t(cluster) * a.K * 8 : 0) + size_t(nst) * NW * 32 * 4;
+  const Spread s = spread<NW>(a.T, cluster, extra, per_sm<NW>(!a.K));
+  a.stages = s.stages;
   const bool ent = a.entropy || a.saved;
   if (a.K)
-    return ent ? launch_rows(logp_kernel<T, true, true>, a, rows, cluster, smem, st, "logprobs")
-               : launch_rows(logp_kernel<T, true, false>, a, rows, cluster, smem, st, "logprobs");
-  return ent ? launch_rows(logp_kernel<T, false, true>, a, rows, cluster, smem, st, "logprobs")
-             : launch_rows(logp_kernel<T, false, false>, a, rows, cluster, smem, st, "logprobs");
+    return ent ? launch_rows<logp_kernel<T, NW, true, true>>(a, s, THREADS, st, "logprobs")
+               : launch_rows<logp_kernel<T, NW, true, false>>(a, s, THREADS, st, "logprobs");
+  return ent ? launch_rows<logp_kernel<T, NW, false, true>>(a, s, THREADS, st, "logprobs")
+             : launch_rows<logp_kernel<T, NW, false, false>>(a, s, THREADS, st, "logprobs");
+}
+template <typename T>
+poet_status run_logp(LogpArgs &a, cudaStream_t st) {
+  const int cluster = cluster_of(a.T, a.V);
+  return a.V <= NARROW ? run_logp<T, 2>(a, cluster, st) : run_logp<T, 8>(a, cluster, st);
 }
 
+template <typename T, int NW>
+poet_status run_distill(DistillArgs &a, int cluster, cudaStream_t st) {
+  constexpr int THREADS = (NW + 2) * 32;
+  const size_t marks = a.tail ? mark_bytes_of<T>(a.V, cluster) : 0;
+  const Spread s = spread<NW>(a.T, cluster, 2 * marks, per_sm<NW>(false));
+  a.stages = s.stages;
+  return a.out ? launch_rows<distill_kernel<T, NW, true>>(a, s, THREADS, st, "distill")
+               : launch_rows<distill_kernel<T, NW, false>>(a, s, THREADS, st, "distill");
+}
 template <typename T>
-poet_status run_distill(const DistillArgs &a, int64_t rows, cudaStream_t st) {
-  const int cluster = cluster_of(rows, a.V);
-  const int nv = a.V / Slice<T>::E / cluster + 1;
-  const size_t smem = a.tail ? size_t(((nv + 2) * Slice<T>::E + 31) / 32) * 4 : 0;
-  return a.out ? launch_rows(distill_kernel<T, true>, a, rows, cluster, smem, st, "distill")
-               : launch_rows(distill_kernel<T, false>, a, rows, cluster, smem, st, "distill");
+poet_status run_distill(DistillArgs &a, cudaStream_t st) {
+  const int cluster = cluster_of(a.T, a.V);
+  return a.V <= NARROW ? run_distill<T, 2>(a, cluster, st) : run_distill<T, 8>(a, cluster, st);
 }
 
 poet_status check_teacher(const char *what, const int32_t *tokens, const float *values, int32_t K, float value_scale,
@@ -965,14 +1538,14 @@ poet_status poet_token_logprobs(const void *logits, int64_t ld, int32_t dtype, i
   POET_REQUIRE(topk ? (top_tokens && top_logp) : (!top_tokens && !top_logp),
                "%s: top_tokens and top_logp go with topk > 0", what);
   LogpArgs a{};
-  a.x = logits; a.ld = ld; a.V = V; a.K = topk; a.scale = scale; a.tokens = tokens;
+  a.x = logits; a.ld = ld; a.T = T; a.V = V; a.K = topk; a.scale = scale; a.tokens = tokens;
   a.logp = logp; a.entropy = entropy; a.top_tokens = top_tokens; a.top_logp = top_logp; a.saved = saved;
   a.errword = device_errword();
   POET_REQUIRE(a.errword != nullptr, "%s: no device status word", what);
   TraceScope ts("logprobs", 6.0 * double(T) * V, double(T) * V * double(esize(dtype)),
                 reinterpret_cast<cudaStream_t>(stream));
-  return dtype == POET_BF16 ? run_logp<bf16>(a, T, reinterpret_cast<cudaStream_t>(stream))
-                            : run_logp<float>(a, T, reinterpret_cast<cudaStream_t>(stream));
+  return dtype == POET_BF16 ? run_logp<bf16>(a, reinterpret_cast<cudaStream_t>(stream))
+                            : run_logp<float>(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 poet_status poet_token_logprobs_grad(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V, float scale,
@@ -1018,15 +1591,15 @@ poet_status poet_distill_topk(const void *logits, int64_t ld, int32_t dtype, int
   POET_REQUIRE(al(saved, 16), "%s: saved not 16-byte aligned", what);
   if (dlogits) POET_TRY(check_out(what, logits, ld, dlogits, ldd, dtype, V));
   DistillArgs a{};
-  a.x = logits; a.out = dlogits; a.ld = ld; a.ldd = ldd; a.V = V; a.K = K; a.tail = tail; a.scale = scale;
+  a.x = logits; a.out = dlogits; a.ld = ld; a.ldd = ldd; a.T = T; a.V = V; a.K = K; a.tail = tail; a.scale = scale;
   a.value_scale = value_scale; a.tokens = teacher_tokens; a.values = teacher_values; a.dloss = dloss;
   a.loss = loss; a.saved = saved;
   a.errword = device_errword();
   POET_REQUIRE(a.errword != nullptr, "%s: no device status word", what);
   TraceScope ts("distill", 10.0 * double(T) * V, (dlogits ? 2.0 : 1.0) * double(T) * V * double(esize(dtype)),
                 reinterpret_cast<cudaStream_t>(stream));
-  return dtype == POET_BF16 ? run_distill<bf16>(a, T, reinterpret_cast<cudaStream_t>(stream))
-                            : run_distill<float>(a, T, reinterpret_cast<cudaStream_t>(stream));
+  return dtype == POET_BF16 ? run_distill<bf16>(a, reinterpret_cast<cudaStream_t>(stream))
+                            : run_distill<float>(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 poet_status poet_distill_topk_grad(const void *logits, int64_t ld, int32_t dtype, int64_t T, int32_t V, float scale,
@@ -1042,7 +1615,7 @@ poet_status poet_distill_topk_grad(const void *logits, int64_t ld, int32_t dtype
   POET_TRY(check_out(what, logits, ld, dlogits, ldd, dtype, V));
   POET_REQUIRE(saved && al(saved, 16), "%s: saved NULL or not 16-byte aligned", what);
   DistillArgs a{};
-  a.x = logits; a.out = dlogits; a.ld = ld; a.ldd = ldd; a.V = V; a.K = K; a.tail = tail; a.scale = scale;
+  a.x = logits; a.out = dlogits; a.ld = ld; a.ldd = ldd; a.T = T; a.V = V; a.K = K; a.tail = tail; a.scale = scale;
   a.value_scale = value_scale; a.tokens = teacher_tokens; a.values = teacher_values; a.dloss = dloss;
   a.saved = const_cast<float *>(saved);
   a.parts = parts_of(T, V);
