@@ -44,6 +44,13 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The aligned part of a row slice: elements [lo, lo + head) one by one, then
 // `nv` 16-byte vectors, then elements [tail0, hi) one by one.
 template <typename T>
@@ -75,41 +82,66 @@ __device__ __forceinline__ Slice<T> slice_of(const T *p, int V, int rank, int si
   return s;
 }
 
-// The running sums of some logits of a row, in pairs, relative to a base that
+// The running sums of some logits of a row, in pairs, relative to a base b that
 // follows their maximum: it is moved only when an exponent would pass RISE, which
 // after a thread's first logits is rare, and the sums' relative errors do not
 // depend on it.
-constexpr float RISE = 8.f;
+//
+// An exponent is c x + k, one fused operation with k = -(b c) rounded: the sums
+// are relative to -k / c instead of b, the same for all of them, so only the
+// operation's own rounding counts, and at() gives the exponent of any other
+// logit to convert by.  For a far base (|b c| >= FAR, where k's rounding alone
+// would move the exponents, no base yet, or a scale so small or large that
+// -2^100 would not do for a masked logit) it is c (x - b).
+constexpr float RISE = 8.f, FAR = 1048576.f;
 struct Run {
-  float m, b;  // the largest, the base
+  float m, b, k;  // the largest, the base
+  bool far;
   float2 s, t;
-  __device__ __forceinline__ void clear() { m = b = -INFINITY; s = t = both(0.f); }
-  __device__ __forceinline__ float base() const { return b == -INFINITY ? 0.f : b; }
-  __device__ __forceinline__ void rebase(float to, float c) {  // to >= b
-    const float d = (b - (to == -INFINITY ? 0.f : to)) * c;
-    const float2 f = both(ex2(d));
-    t = mul2(fma2(s, both(fmaxf(d, LOWEST)), t), f);
+  __device__ __forceinline__ void clear() {
+    m = b = -INFINITY;
+    k = 0.f;
+    far = true;
+    s = t = both(0.f);
+  }
+  // the base for far exponents; without a base there are only masked logits
+  __device__ __forceinline__ float origin() const { return b == -INFINITY ? 0.f : b; }
+  __device__ __forceinline__ float at(float x, float c) const { return far ? (x - b) * c : fmaf(x, c, k); }
+  // Moves the sums by D >= 0 (about) towards a larger base.
+  __device__ __forceinline__ void shift(float D) {
+    D = D < -LOWEST ? D : -LOWEST;  // no base yet: the sums are 0
+    const float2 f = both(ex2(-D));
+    t = mul2(fma2(s, both(-D), t), f);
     s = mul2(s, f);
-    b = to;
   }
   // Takes mx into the maximum; call before adding logits up to mx.
   __device__ __forceinline__ void see(float mx, float c) {
     m = fmaxf(m, mx);
-    if ((mx - b) * c > RISE) rebase(mx, c);
-  }
-  // Adds exp(d) and exp(d) d; LOW: some d may be -inf.
-  template <bool ENT, bool LOW>
-  __device__ __forceinline__ void add(float2 x, float2 minus_base, float2 c) {
-    float2 d = mul2(add2(x, minus_base), c);
-    const float2 e = ex2(d);
-    s = add2(s, e);
-    if (ENT) {
-      if (LOW) d = make_float2(fmaxf(d.x, LOWEST), fmaxf(d.y, LOWEST));
-      t = fma2(e, d, t);
+    const float d = at(mx, c);
+    if (d > RISE) {
+      b = mx;
+      k = -(mx * c);
+      far = !(fabsf(k) < FAR && c > 0x1p-60f && c < 0x1p27f);
+      shift(d - (far ? 0.f : fmaf(mx, c, k)));
     }
   }
+  // Adds exp(d) and exp(d) d for two logits.  Near: no logit below -2^100, k2 = k.
+  template <bool ENT>
+  __device__ __forceinline__ void add_near(float2 x, float2 k2, float2 c) {
+    const float2 d = fma2(x, c, k2);
+    const float2 e = ex2(d);
+    s = add2(s, e);
+    if (ENT) t = fma2(e, d, t);
+  }
+  template <bool ENT>
+  __device__ __forceinline__ void add_far(float2 x, float2 minus_b, float2 c) {
+    const float2 d = mul2(add2(x, minus_b), c);
+    const float2 e = ex2(d);
+    s = add2(s, e);
+    if (ENT) t = fma2(e, make_float2(fmaxf(d.x, LOWEST), fmaxf(d.y, LOWEST)), t);
+  }
   __device__ __forceinline__ void add1(float x, float c) {
-    const float d = (x - base()) * c, e = ex2(d);
+    const float d = far ? (x - origin()) * c : fmaf(x, c, k), e = ex2(d);
     s.x += e;
     t.x = fmaf(e, fmaxf(d, LOWEST), t.x);
   }
@@ -148,7 +180,7 @@ __device__ __forceinline__ Sums join_lanes(Sums a, float c) {
 }
 __device__ __forceinline__ Sums join_warp(Run &r, float c) {
   const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(r.m)));
-  r.rebase(m, c);
+  if (m > -INFINITY) r.shift(r.at(m, c));
   float v[2] = {r.s.x + r.s.y, r.t.x + r.t.y};
   row_sum<2>(v, nullptr, 1, 0, 0, 32);
   return {m, v[0], v[1]};
@@ -161,18 +193,23 @@ template <>
 struct Vec<bf16> {
   static constexpr int E = 8;
   static constexpr uint32_t MASKED = 0xff80ff80u;
+  // no element below -2^100; NaN stays
+  static __device__ __forceinline__ uint4 bounded(const uint4 &v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Top t = __hmax2_nan(word(w[i]), word(0xf180f180u));
+      w[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
   using Top = __nv_bfloat162;
   static __device__ __forceinline__ Top word(uint32_t w) { return *reinterpret_cast<const Top *>(&w); }
   static __device__ __forceinline__ Top largest(const uint4 &v) {
     return __hmax2(__hmax2(word(v.x), word(v.y)), __hmax2(word(v.z), word(v.w)));
   }
-  static __device__ __forceinline__ Top smallest(const uint4 &v) {
-    return __hmin2(__hmin2(word(v.x), word(v.y)), __hmin2(word(v.z), word(v.w)));
-  }
   static __device__ __forceinline__ Top larger(Top a, Top b) { return __hmax2(a, b); }
-  static __device__ __forceinline__ Top smaller(Top a, Top b) { return __hmin2(a, b); }
   static __device__ __forceinline__ float top(Top a) { return fmaxf(__low2float(a), __high2float(a)); }
-  static __device__ __forceinline__ float bottom(Top a) { return fminf(__low2float(a), __high2float(a)); }
   static __device__ __forceinline__ void get(const uint4 &v, float2 (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -202,18 +239,17 @@ template <>
 struct Vec<float> {
   static constexpr int E = 4;
   static constexpr uint32_t MASKED = 0xff800000u;
+  static __device__ __forceinline__ uint4 bounded(const uint4 &v) {
+    auto g = [](uint32_t w) { return __float_as_uint(max_nan(f(w), -0x1p100f)); };
+    return make_uint4(g(v.x), g(v.y), g(v.z), g(v.w));
+  }
   using Top = float;
   static __device__ __forceinline__ float f(uint32_t w) { return __uint_as_float(w); }
   static __device__ __forceinline__ Top largest(const uint4 &v) {
     return fmaxf(fmaxf(f(v.x), f(v.y)), fmaxf(f(v.z), f(v.w)));
   }
-  static __device__ __forceinline__ Top smallest(const uint4 &v) {
-    return fminf(fminf(f(v.x), f(v.y)), fminf(f(v.z), f(v.w)));
-  }
   static __device__ __forceinline__ Top larger(Top a, Top b) { return fmaxf(a, b); }
-  static __device__ __forceinline__ Top smaller(Top a, Top b) { return fminf(a, b); }
   static __device__ __forceinline__ float top(Top a) { return a; }
-  static __device__ __forceinline__ float bottom(Top a) { return a; }
   static __device__ __forceinline__ void get(const uint4 &v, float2 (&x)[2]) {
     x[0] = make_float2(f(v.x), f(v.y));
     x[1] = make_float2(f(v.z), f(v.w));
@@ -335,17 +371,21 @@ struct Spot {
 
 // The producer: one thread copies the vectors of every row's slice, NW * 32 * U
 // at a time, into the ring; `passes` times each row (a second time where a row
-// does not fit the ring and is read again for its gradient).  live(row): whether
-// the row is read at all (the whole warp calls it).
+// does not fit the ring and is read again for its gradient).  rows.fetch(row)
+// loads what decides whether a row is read at all, a row ahead, and rows.live()
+// decides (the whole warp calls both).
 template <typename T, int NW, typename F>
 __device__ void produce(Pipe &P, const unsigned char *ring, int stages, const void *x0, int64_t ld, int V, int64_t T_rows,
-                        int64_t first, int64_t step, int rank, int size, bool twice, unsigned *errword, F live) {
+                        int64_t first, int64_t step, int rank, int size, bool twice, unsigned *errword, F rows) {
   constexpr int SV = NW * 32 * U;
   Spot at;
   int64_t issued = 0;
   bool ok = true;
+  if (first < T_rows) rows.fetch(first);
   for (int64_t row = first; row < T_rows && ok; row += step) {
-    if (!live(row)) continue;
+    const bool live = rows.live();
+    if (row + step < T_rows) rows.fetch(row + step);
+    if (!live) continue;
     const T *x = static_cast<const T *>(x0) + row * ld;
     const Slice<T> sl = slice_of(x, V, rank, size);
     const T *body = x + sl.lo + sl.head;
@@ -410,24 +450,24 @@ __device__ __forceinline__ float add_vectors(Run &r, const uint4 (&v)[U], float 
   for (int u = 1; u < U; ++u) hi = X::larger(hi, X::largest(v[u]));
   const float mx = X::top(hi);
   r.see(mx, c);
-  bool low = false;
-  if (ENT) {  // may an exponent be -inf?
-    typename X::Top lo = X::smallest(v[0]);
+  const float2 c2 = both(c);
+  if (!r.far) {
+    const float2 k2 = both(r.k);
 #pragma unroll
-    for (int u = 1; u < U; ++u) lo = X::smaller(lo, X::smallest(v[u]));
-    low = !((X::bottom(lo) - r.base()) * c > LOWEST);
-  }
-  const float2 mb = both(-r.base()), c2 = both(c);
+    for (int u = 0; u < U; ++u) {
+      float2 x[X::E / 2];
+      X::get(ENT ? X::bounded(v[u]) : v[u], x);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float2 x[X::E / 2];
-    X::get(v[u], x);
-    if (ENT && low) {
+      for (int i = 0; i < X::E / 2; ++i) r.template add_near<ENT>(x[i], k2, c2);
+    }
+  } else {
+    const float2 mb = both(-r.origin());
 #pragma unroll
-      for (int i = 0; i < X::E / 2; ++i) r.add<ENT, true>(x[i], mb, c2);
-    } else {
+    for (int u = 0; u < U; ++u) {
+      float2 x[X::E / 2];
+      X::get(v[u], x);
 #pragma unroll
-      for (int i = 0; i < X::E / 2; ++i) r.add<ENT, false>(x[i], mb, c2);
+      for (int i = 0; i < X::E / 2; ++i) r.template add_far<ENT>(x[i], mb, c2);
     }
   }
   return mx;
@@ -698,6 +738,13 @@ struct LogpArgs {
   unsigned *errword;
 };
 
+struct GivenTokens {
+  const int32_t *tokens;
+  int V, token;
+  __device__ __forceinline__ void fetch(int64_t row) { token = tokens ? tokens[row] : 0; }
+  __device__ __forceinline__ bool live() const { return token >= 0 && token < V; }
+};
+
 // The computing warps' part.
 template <typename T, int NW, bool TOP, bool ENT>
 __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, unsigned char *ring, int rank, int size,
@@ -841,10 +888,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, per_sm<NW>(!TOP)) logp_kernel(c
   const int64_t first = blockIdx.x / size, step = gridDim.x / size;
   pipe_init<NW>(P, a.stages, size, cl);
   if (threadIdx.x >= NW * 32)
-    produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, false, a.errword, [&](int64_t row) {
-      const int t = a.tokens ? a.tokens[row] : 0;
-      return t >= 0 && t < a.V;
-    });
+    produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, false, a.errword,
+                   GivenTokens{a.tokens, a.V, 0});
   else
     logp_rows<T, NW, TOP, ENT>(a, P, ring, rank, size, first, step);
   if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
@@ -977,7 +1022,9 @@ struct DistillArgs {
 };
 
 // A row's teacher entries in shared memory.
+constexpr int HASH = 256;
 struct Teacher {
+  int hash[HASH];    // -1 between rows
   float q[MAX_K], lq[MAX_K], x[MAX_K];
   float sum[MAX_K];  // of a token's first entry: the q of all its entries
   int idx[MAX_K];    // -1: left out
@@ -991,11 +1038,30 @@ struct Teacher {
   unsigned head, behind;
 };
 
-// Loads the entries, their probabilities q and ln q, and the student's logits
-// at those in [lo, hi).  One warp.
-template <typename T>
-__device__ void load_teacher(Teacher &S, const DistillArgs &a, int64_t row, const T *x, int lo, int hi, bool report) {
-  constexpr int Q = MAX_K / 32;  // entries of a lane
+// A row's entries as they are given, some to each lane of a warp, and the
+// student's logits at those in [lo, hi).
+struct Entries {
+  static constexpr int Q = MAX_K / 32;  // entries of a lane: lane, lane + 32, ...
+  int t[Q];
+  float v[Q], x[Q];
+  __device__ __forceinline__ void fetch(const DistillArgs &a, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const int k = int(threadIdx.x & 31) + 32 * i;
+      t[i] = k < a.K ? a.tokens[row * a.K + k] : -1;
+      v[i] = k < a.K ? a.values[row * a.K + k] : 0.f;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void gather(const T *row, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < Q; ++i) x[i] = t[i] >= lo && t[i] < hi ? to_float(row[t[i]]) : -INFINITY;
+  }
+};
+
+// The entries' probabilities q and ln q.  One warp.
+__device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, const Entries &e, bool report) {
+  constexpr int Q = Entries::Q;
   const int lane = threadIdx.x & 31;
   const float c = a.scale * LOG2E;
   int t[Q];
@@ -1004,22 +1070,14 @@ __device__ void load_teacher(Teacher &S, const DistillArgs &a, int64_t row, cons
   int n = 0;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    const int k = lane + 32 * i;
-    t[i] = -1;
-    lq[i] = xs[i] = -INFINITY;
-    if (k < a.K) {
-      t[i] = a.tokens[row * a.K + k];
-      lq[i] = a.values[row * a.K + k] * a.value_scale;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < Q; ++i) {
+    t[i] = e.t[i];
+    xs[i] = e.x[i];
+    lq[i] = e.v[i] * a.value_scale;
     if (t[i] >= a.V && report) atomicOr(a.errword, unsigned(ERR_BOUNDS));
     if (t[i] < 0 || t[i] >= a.V) {
       t[i] = -1;
       lq[i] = -INFINITY;
     }
-    if (t[i] >= lo && t[i] < hi) xs[i] = to_float(x[t[i]]);
     if (lane + 32 * i < a.K) S.idx[lane + 32 * i] = t[i];
     mx = fmaxf(mx, lq[i]);
     n += t[i] >= 0;
@@ -1050,15 +1108,31 @@ __device__ void load_teacher(Teacher &S, const DistillArgs &a, int64_t row, cons
     }
   }
   __syncwarp();
-  // a token's first entry, and the sum over all its entries
+  // a token's first entry, and the sum over all its entries: every entry's own unless a hash table (empty between
+  // rows, at most half full) shows that a token is listed twice
   float sum[Q];
-  bool first[Q];
+  bool first[Q], twice = false;
+  int slot[Q];
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    sum[i] = 0.f;
     first[i] = t[i] >= 0;
+    sum[i] = q[i];
+    slot[i] = -1;
+    if (!first[i]) continue;
+    for (int h = int((unsigned(t[i]) * 2654435761u) >> 24);; h = (h + 1) % HASH) {
+      const int was = atomicCAS(&S.hash[h], -1, t[i]);
+      if (was == -1) slot[i] = h;
+      if (was == t[i]) twice = true;
+      if (was == -1 || was == t[i]) break;
+    }
   }
-  for (int j = 0; j < a.K; ++j) {
+  twice = __any_sync(0xffffffffu, twice);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    if (slot[i] >= 0) S.hash[slot[i]] = -1;
+    if (twice) sum[i] = 0.f;
+  }
+  for (int j = 0; twice && j < a.K; ++j) {
     const int tj = S.idx[j];
     const float qj = S.q[j];
 #pragma unroll
@@ -1129,16 +1203,19 @@ __device__ __forceinline__ Outside outside_of(const Teacher &S, int tail, float 
   return o;
 }
 
-// Whether a row has a teacher (the same decision as load_teacher's live), by one warp.
-__device__ __forceinline__ bool has_teacher(const DistillArgs &a, int64_t row) {
-  bool any = false;
-  for (int k = threadIdx.x & 31; k < a.K; k += 32) {
-    const int t = a.tokens[row * a.K + k];
-    const float v = a.values[row * a.K + k] * a.value_scale;
-    any = any || (t >= 0 && t < a.V && (a.tail || v != -INFINITY));
+// Whether a row has a teacher: the same decision as load_teacher's live.
+struct HasTeacher {
+  const DistillArgs &a;
+  Entries e;
+  __device__ __forceinline__ void fetch(int64_t row) { e.fetch(a, row); }
+  __device__ __forceinline__ bool live() const {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < Entries::Q; ++i)
+      any = any || (e.t[i] >= 0 && e.t[i] < a.V && (a.tail || e.v[i] * a.value_scale != -INFINITY));
+    return __any_sync(0xffffffffu, any);
   }
-  return __any_sync(0xffffffffu, any);
-}
+};
 
 // The marks of a slice's vectors, a byte each.
 template <typename T>
@@ -1149,9 +1226,23 @@ template <typename T>
 __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teacher (&teachers)[2], unsigned char *marks,
                                              int mark_bytes, int rank, int size, int64_t first, int64_t step) {
   constexpr int E = Vec<T>::E;
+  // the entries are loaded two rows ahead, the logits at them one
+  const T *x0 = static_cast<const T *>(a.x);
+  Entries e, ahead;
+  if (first < a.T) {
+    e.fetch(a, first);
+    e.gather(x0 + first * a.ld, 0, a.V);
+    if (first + step < a.T) ahead.fetch(a, first + step);
+  }
   int64_t n = 0;
   for (int64_t row = first; row < a.T; row += step, ++n) {
     Teacher &S = teachers[n & 1];
+    const Entries now = e;
+    if (row + step < a.T) {
+      e = ahead;
+      e.gather(x0 + (row + step) * a.ld, 0, a.V);
+      if (row + 2 * step < a.T) ahead.fetch(a, row + 2 * step);
+    }
     bar_wait(&P.tempty[n & 1], uint32_t(n >> 1 & 1) ^ 1, &P.abort, a.errword);
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
     unsigned *words = reinterpret_cast<unsigned *>(marks + (n & 1) * mark_bytes);
@@ -1162,7 +1253,7 @@ __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teac
         if (S.nv && S.idx[k] >= 0 && i >= 0 && i < S.nv * E) words[i / E / 4] = 0u;
       }
     __syncwarp();
-    load_teacher(S, a, row, x, 0, a.V, rank == 0);
+    load_teacher(S, a, now, rank == 0);
     if (a.tail) {
       const Slice<T> sl = slice_of(x, a.V, rank, size);
       const int base = sl.lo + sl.head;
@@ -1286,13 +1377,21 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
       if (bad) o.f = NAN;
       // a row of masks: 0 everywhere
       const float A = empty ? 0.f : o.f * g, L = empty ? 0.f : o.L * LOG2E, base = empty ? 0.f : M;
-      const float2 A2 = both(A), nL = both(-L), nM = both(-base), c2 = both(c);
-      auto grad = [&](float v) { return A * ex2(fmaf(v - base, c, -L)); };
+      // the exponent c (v - M) - L as c v + k, with what k's rounding leaves taken into the factor; where M is far,
+      // in two steps
+      const bool far = !(fabsf(base * c) < FAR);
+      const float mc = base * c, k = -mc - L, kb = k + mc;
+      const float left = fmaf(-base, c, mc) + ((-mc - (k - kb)) + (-L - kb));  // -base c - L - k
+      const float2 A2 = both(far ? A : A * ex2(left)), k2 = both(far ? -base : k), nL = both(-L), c2 = both(c);
+      auto grad = [&](float2 v) {
+        const float2 d = far ? fma2(add2(v, k2), c2, nL) : fma2(v, c2, k2);
+        return mul2(ex2(d), A2);
+      };
       T *to = out + sl.lo + sl.head;
       const bool aligned = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
       if (tid < 32) {
-        if (tid < sl.head) out[sl.lo + tid] = from_float<T>(grad(xh));
-        if (sl.tail0 + tid < sl.hi) out[sl.tail0 + tid] = from_float<T>(grad(xt));
+        if (tid < sl.head) out[sl.lo + tid] = from_float<T>(grad(both(xh)).x);
+        if (sl.tail0 + tid < sl.hi) out[sl.tail0 + tid] = from_float<T>(grad(both(xt)).x);
       }
       Spot &from = stays ? again : at;
       for (int k = 0; k < nst; ++k) {
@@ -1309,7 +1408,7 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
           float2 f[E / 2];
           Vec<T>::get(v[u], f);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) f[e] = mul2(ex2(fma2(add2(f[e], nM), c2, nL)), A2);
+          for (int e = 0; e < E / 2; ++e) f[e] = grad(f[e]);
           if (aligned) {
             *reinterpret_cast<uint4 *>(to + int64_t(i) * E) = Vec<T>::put(f);
           } else {
@@ -1345,12 +1444,13 @@ __global__ void __launch_bounds__((NW + 2) * 32, per_sm<NW>(false)) distill_kern
   unsigned char *marks = ring + a.stages * (G * U * 16);
   for (int i = tid; i < 2 * mark_bytes / 4; i += (NW + 2) * 32) reinterpret_cast<unsigned *>(marks)[i] = 0u;
   if (tid < 2) teachers[tid].nv = 0;
+  for (int i = tid; i < 2 * HASH; i += (NW + 2) * 32) teachers[i / HASH].hash[i % HASH] = -1;
   pipe_init<NW>(P, a.stages, size, cl);
   if (tid >= G + 32)
     teacher_rows<T>(a, P, teachers, marks, mark_bytes, rank, size, first, step);
   else if (tid >= G)
     produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, GRAD, a.errword,
-                   [&](int64_t row) { return has_teacher(a, row); });
+                   HasTeacher{a, {}});
   else
     distill_rows<T, NW, GRAD>(a, P, teachers, ring, marks, mark_bytes, rank, size, first, step);
   if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
@@ -1364,8 +1464,15 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
   const T *x = static_cast<const T *>(a.x) + row * a.ld;
   T *out = static_cast<T *>(a.out) + row * a.ldd;
   const Slice<T> sl = slice_of(x, a.V, part, a.parts);
+  for (int i = threadIdx.x; i < HASH; i += NT) S.hash[i] = -1;
+  __syncthreads();
   // only this part's logits: in place, the other parts may already be gradients
-  if (threadIdx.x < 32) load_teacher(S, a, row, x, sl.lo, sl.hi, part == 0);
+  if (threadIdx.x < 32) {
+    Entries e;
+    e.fetch(a, row);
+    e.gather(x, sl.lo, sl.hi);
+    load_teacher(S, a, e, part == 0);
+  }
   __syncthreads();
   const float4 sv = reinterpret_cast<const float4 *>(a.saved)[row];
   if (S.live == 0 || sv.x == -INFINITY) {
