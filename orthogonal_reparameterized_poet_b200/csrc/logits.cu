@@ -1089,18 +1089,19 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    q[i] = t[i] >= 0 ? expf(lq[i] - mx) : 0.f;
+    q[i] = 0.f;
+    if (32 * i < a.K && t[i] >= 0) q[i] = expf(lq[i] - mx);
     s += q[i];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (!a.tail && s == 0.f) n = 0;  // nothing but -inf: no teacher
-  const float ls = a.tail ? 0.f : mx + logf(s);
+  const float ls = a.tail ? 0.f : mx + logf(s), inv_s = n ? 1.f / s : 0.f;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int k = lane + 32 * i;
     lq[i] -= ls;
-    if (!a.tail) q[i] = n ? q[i] / s : 0.f;
+    if (!a.tail) q[i] *= inv_s;
     if (k < a.K) {
       S.q[k] = q[i];
       S.lq[k] = lq[i];
@@ -1118,7 +1119,7 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
     first[i] = t[i] >= 0;
     sum[i] = q[i];
     slot[i] = -1;
-    if (!first[i]) continue;
+    if (32 * i >= a.K || !first[i]) continue;
     for (int h = int((unsigned(t[i]) * 2654435761u) >> 24);; h = (h + 1) % HASH) {
       const int was = atomicCAS(&S.hash[h], -1, t[i]);
       if (was == -1) slot[i] = h;
@@ -1221,11 +1222,17 @@ struct HasTeacher {
 template <typename T>
 __host__ __device__ inline int mark_bytes_of(int V, int size) { return (V / Vec<T>::E / size + 2 + 15) / 16 * 16; }
 
-// One warp's part: the teacher's entries of the rows to come.
+// The part of two warps, every second row each: the teacher's entries of the
+// rows to come (one warp alone would hold up the others: a row's entries are a
+// long chain of few instructions).
 template <typename T>
 __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teacher (&teachers)[2], unsigned char *marks,
-                                             int mark_bytes, int rank, int size, int64_t first, int64_t step) {
+                                             int mark_bytes, int rank, int size, int64_t first, int64_t step, int odd) {
   constexpr int E = Vec<T>::E;
+  first += odd * step;
+  step *= 2;
+  Teacher &S = teachers[odd];
+  unsigned *words = reinterpret_cast<unsigned *>(marks + odd * mark_bytes);
   // the entries are loaded two rows ahead, the logits at them one
   const T *x0 = static_cast<const T *>(a.x);
   Entries e, ahead;
@@ -1234,18 +1241,16 @@ __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teac
     e.gather(x0 + first * a.ld, 0, a.V);
     if (first + step < a.T) ahead.fetch(a, first + step);
   }
-  int64_t n = 0;
-  for (int64_t row = first; row < a.T; row += step, ++n) {
-    Teacher &S = teachers[n & 1];
+  uint32_t phase = 1;
+  for (int64_t row = first; row < a.T; row += step, phase ^= 1) {
     const Entries now = e;
     if (row + step < a.T) {
       e = ahead;
       e.gather(x0 + (row + step) * a.ld, 0, a.V);
       if (row + 2 * step < a.T) ahead.fetch(a, row + 2 * step);
     }
-    bar_wait(&P.tempty[n & 1], uint32_t(n >> 1 & 1) ^ 1, &P.abort, a.errword);
+    bar_wait(&P.tempty[odd], phase, &P.abort, a.errword);
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
-    unsigned *words = reinterpret_cast<unsigned *>(marks + (n & 1) * mark_bytes);
     const int lane = threadIdx.x & 31;
     if (a.tail)  // the marks of the buffer's last row
       for (int k = lane; k < a.K; k += 32) {
@@ -1276,7 +1281,7 @@ __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teac
       }
     }
     __syncwarp();
-    if (lane == 0) bar_arrive(&P.tfull[n & 1]);
+    if (lane == 0) bar_arrive(&P.tfull[odd]);
   }
 }
 
@@ -1424,14 +1429,14 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
   }
 }
 
-// NW warps compute, one streams the rows, one loads the teacher's entries of
-// the rows to come.  With the tail as one more outcome the sum runs over the
+// NW warps compute, one streams the rows, two load the teacher's entries of the
+// rows to come.  With the tail as one more outcome the sum runs over the
 // tokens outside the teacher's alone (they may be all that is left of 1 in
 // float), so the teacher's are marked, a bit each, and masked as they are read.
 // A row whose slice fits the ring stays there for its gradient; a longer one is
 // streamed a second time (from L2).
 template <typename T, int NW, bool GRAD>
-__global__ void __launch_bounds__((NW + 2) * 32, per_sm<NW>(false)) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__((NW + 3) * 32, per_sm<NW>(false)) distill_kernel(const DistillArgs a) {
   constexpr int G = NW * 32;
   __shared__ Pipe P;
   __shared__ Teacher teachers[2];
@@ -1442,12 +1447,12 @@ __global__ void __launch_bounds__((NW + 2) * 32, per_sm<NW>(false)) distill_kern
   const int tid = threadIdx.x;
   const int mark_bytes = a.tail ? mark_bytes_of<T>(a.V, size) : 0;
   unsigned char *marks = ring + a.stages * (G * U * 16);
-  for (int i = tid; i < 2 * mark_bytes / 4; i += (NW + 2) * 32) reinterpret_cast<unsigned *>(marks)[i] = 0u;
+  for (int i = tid; i < 2 * mark_bytes / 4; i += (NW + 3) * 32) reinterpret_cast<unsigned *>(marks)[i] = 0u;
   if (tid < 2) teachers[tid].nv = 0;
-  for (int i = tid; i < 2 * HASH; i += (NW + 2) * 32) teachers[i / HASH].hash[i % HASH] = -1;
+  for (int i = tid; i < 2 * HASH; i += (NW + 3) * 32) teachers[i / HASH].hash[i % HASH] = -1;
   pipe_init<NW>(P, a.stages, size, cl);
   if (tid >= G + 32)
-    teacher_rows<T>(a, P, teachers, marks, mark_bytes, rank, size, first, step);
+    teacher_rows<T>(a, P, teachers, marks, mark_bytes, rank, size, first, step, (tid - G - 32) / 32);
   else if (tid >= G)
     produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, GRAD, a.errword,
                    HasTeacher{a, {}});
@@ -1597,7 +1602,7 @@ poet_status run_logp(LogpArgs &a, cudaStream_t st) {
 
 template <typename T, int NW>
 poet_status run_distill(DistillArgs &a, int cluster, cudaStream_t st) {
-  constexpr int THREADS = (NW + 2) * 32;
+  constexpr int THREADS = (NW + 3) * 32;
   const size_t marks = a.tail ? mark_bytes_of<T>(a.V, cluster) : 0;
   const Spread s = spread<NW>(a.T, cluster, 2 * marks, per_sm<NW>(false));
   a.stages = s.stages;
