@@ -678,9 +678,14 @@ def _dtype_of(t, what):
     raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
 
 
+def _plain(t, shape, dtype, device):
+    """Whether t is a contiguous tensor of this shape and type on that device: what nearly every operand is."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
 def _operand(t, name, shape, dtype, device, rows=True):
     """A device operand: its address and row stride (rows contiguous), after checks.  device: its index."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+    if _plain(t, shape, dtype, device):
         return t.data_ptr(), shape[-1]
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
@@ -714,30 +719,34 @@ def _stream_on(stream, device):
     return stream.cuda_stream
 
 
-def _new(shape, dtype, device, stream):
-    """A new contiguous tensor that belongs to the stream that the call runs on."""
+def _new(shape, dtype, device, stream, like=None):
+    """A new contiguous tensor that belongs to the stream that the call runs on.  like: a contiguous tensor of the
+    same shape, type and device, where there is one at hand."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(like) if like is not None else torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 _MAXI32 = 2**31 - 1
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps):
     """The poet_joint of these options, with the addresses and strides of o, h and the gate."""
-    if h.dim() != 2:
+    shape = h.shape
+    if len(shape) != 2:
         raise ValueError("h must be 2-D (tokens x width)")
     dev = _current(h, "h")
-    shape = T, d = h.shape
+    T, d = shape
     t = h.dtype
+    dt = _dtype_of(h, "h")
     ph, ldh = _operand(h, "h", shape, t, dev)
     kind, po, ldo, pg, ldg, pq, pn = GATE_NONE, None, 0, None, 0, None, None
     if o is not None:
         po, ldo = _operand(o, "o", shape, t, dev)
         if w_post is not None:
-            pq = _operand(w_post, "w_post", (d,), torch.float32, dev, False)[0]
+            pq = _operand(w_post, "w_post", (d,), _F32, dev, False)[0]
         if gate is not None:
             if gate_rows < 1:
                 raise ValueError("gate_rows must be at least 1")
@@ -751,10 +760,11 @@ def _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, bet
     elif gate is not None or w_post is not None:
         raise ValueError("a gate and w_post need o")
     if w_pre is not None:
-        pn = _operand(w_pre, "w_pre", (d,), torch.float32, dev, False)[0]
-    J = poet_joint(d if d <= _MAXI32 else _MAXI32, _dtype_of(h, "h"), 1 if post_norm and o is not None else 0, kind,
-                   gate_act, 0, gate_rows, alpha, beta, eps, pq, pn)
-    return J, dev, shape, t, po, ldo, ph, ldh, pg, ldg
+        pn = _operand(w_pre, "w_pre", (d,), _F32, dev, False)[0]
+    J = poet_joint(d if d <= _MAXI32 else _MAXI32, dt, 1 if post_norm and o is not None else 0, kind, gate_act, 0,
+                   gate_rows, alpha, beta, eps, pq, pn)
+    # a contiguous h serves as the pattern of what is allocated
+    return J, dev, shape, t, po, ldo, ph, ldh, pg, ldg, (h if ldh == d and h.is_contiguous() else None)
 
 
 def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, pre_norm=True, gate_act=GATE_LINEAR,
@@ -766,24 +776,25 @@ def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, p
     takes o as it is; pre_norm=False leaves n out (None).  o=None: n = rmsnorm(h) w_pre alone (h' is None).
     h_out and n are allocated where they are not given.  stream: the stream to run on (None: the current one);
     what is allocated belongs to it."""
-    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows,
-                                                         alpha, beta, eps)
+    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg, like = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act,
+                                                               gate_rows, alpha, beta, eps)
     if o is None and (h_out is not None or not pre_norm):
         raise ValueError("without o there is only n")
     if not pre_norm and (n is not None or w_pre is not None):
         raise ValueError("n and w_pre need pre_norm")
     st = _stream_on(stream, dev)
+    d = shape[1]
     pho, ldho, pn, ldn = None, 0, None, 0
     if h_out is not None:
         pho, ldho = _operand(h_out, "h_out", shape, t, dev)
     elif o is not None:
-        h_out = _new(shape, t, dev, stream)
-        pho, ldho = h_out.data_ptr(), shape[1]
+        h_out = _new(shape, t, dev, stream, like)
+        pho, ldho = h_out.data_ptr(), d
     if n is not None:
         pn, ldn = _operand(n, "n", shape, t, dev)
     elif pre_norm:
-        n = _new(shape, t, dev, stream)
-        pn, ldn = n.data_ptr(), shape[1]
+        n = _new(shape, t, dev, stream, like)
+        pn, ldn = n.data_ptr(), d
     _check(lib().poet_joint_forward(ctypes.byref(J), po, ldo, ph, ldh, pg, ldg, shape[0], pho, ldho, pn, ldn, st))
     return h_out, n
 
@@ -801,9 +812,8 @@ def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_
     be None).  o, gate and the options are the forward's, h_out its result (h where o is None).  Gradients of
     what the joint does not have are None; the others are allocated where they are not given (ws too).  Two
     calls that may run at the same time need a ws each."""
-    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows,
-                                                         alpha, beta, eps)
-    d = shape[1]
+    J, dev, shape, t, po, ldo, ph, ldh, pg, ldg, like = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act,
+                                                               gate_rows, alpha, beta, eps)
     if dn is None and w_pre is not None:
         raise ValueError("w_pre needs dn")
     for name, have, want in (("d_o", d_o, o), ("dgate", dgate, gate), ("dw_post", dw_post, w_post),
@@ -811,31 +821,51 @@ def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_
         if have is not None and want is None:
             raise ValueError(f"{name} is the gradient of something this joint does not have")
     st = _stream_on(stream, dev)
-
-    def result(x, name, shape, dtype, of):
-        """A gradient (x, or a new one where `of` is there), its address and row stride."""
-        if x is not None:
-            return (x, *_operand(x, name, shape, dtype, dev, len(shape) == 2))
-        if of is None:
-            return None, None, 0
-        x = _new(shape, dtype, dev, stream)
-        return x, x.data_ptr(), shape[-1]
-
-    pd, ldd = _operand(dh_out, "dh_out", shape, t, dev) if dh_out is not None else (None, 0)
-    pn, ldn = _operand(dn, "dn", shape, t, dev) if dn is not None else (None, 0)
-    dh, pdh, lddh = result(dh, "dh", shape, t, h_out)
-    d_o, pdo, lddo = result(d_o, "d_o", shape, t, o)
-    dgate, pdg, lddg = result(dgate, "dgate", gate.shape if gate is not None else None, t, gate)
-    if gate is not None and gate.dim() == 1:
-        lddg = 1
-    dw_post, pwq, _ = result(dw_post, "dw_post", (d,), torch.float32, w_post)
-    dw_pre, pwn, _ = result(dw_pre, "dw_pre", (d,), torch.float32, w_pre)
+    T, d = shape
+    pd = pn = pdo = pdg = pwq = pwn = None
+    ldd = ldn = lddo = lddg = 0
+    if dh_out is not None:
+        pd, ldd = _operand(dh_out, "dh_out", shape, t, dev)
+    if dn is not None:
+        pn, ldn = _operand(dn, "dn", shape, t, dev)
+    if dh is None:
+        dh = _new(shape, t, dev, stream, like)
+        pdh, lddh = dh.data_ptr(), d
+    else:
+        pdh, lddh = _operand(dh, "dh", shape, t, dev)
+    if o is not None:
+        if d_o is None:
+            d_o = _new(shape, t, dev, stream, like)
+            pdo, lddo = d_o.data_ptr(), d
+        else:
+            pdo, lddo = _operand(d_o, "d_o", shape, t, dev)
+    if gate is not None:
+        if dgate is None:
+            dgate = _new(gate.shape, t, dev, stream)
+            pdg, lddg = dgate.data_ptr(), d
+        else:
+            pdg, lddg = _operand(dgate, "dgate", gate.shape, t, dev, gate.dim() == 2)
+        if gate.dim() == 1:
+            lddg = 1
+    if w_post is not None:
+        if dw_post is None:
+            dw_post = _new((d,), _F32, dev, stream)
+            pwq = dw_post.data_ptr()
+        else:
+            pwq = _operand(dw_post, "dw_post", (d,), _F32, dev, False)[0]
+    if w_pre is not None:
+        if dw_pre is None:
+            dw_pre = _new((d,), _F32, dev, stream)
+            pwn = dw_pre.data_ptr()
+        else:
+            pwn = _operand(dw_pre, "dw_pre", (d,), _F32, dev, False)[0]
+    J_at = ctypes.byref(J)
     if ws is None:
-        ws = _new((max(lib().poet_joint_workspace_bytes(ctypes.byref(J), shape[0]), 1),), torch.uint8, dev, stream)
+        ws = _new((lib().poet_joint_workspace_bytes(J_at, T) or 1,), torch.uint8, dev, stream)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}, not on cuda:{dev}")
-    _check(lib().poet_joint_backward(ctypes.byref(J), po, ldo, ph, ldh, pg, ldg, pd, ldd, pn, ldn, shape[0], pdh, lddh,
-                                     pdo, lddo, pdg, lddg, pwq, pwn, ws.data_ptr(), ws.nbytes, st))
+    _check(lib().poet_joint_backward(J_at, po, ldo, ph, ldh, pg, ldg, pd, ldd, pn, ldn, T, pdh, lddh, pdo, lddo, pdg,
+                                     lddg, pwq, pwn, ws.data_ptr(), ws.nbytes, st))
     return dh, d_o, dgate, dw_post, dw_pre
 
 
@@ -856,10 +886,19 @@ def _per_row(x, name, T, dtype, dev):
     return None if x is None else _operand(x, name, (T,), dtype, dev, False)[0]
 
 
+def _saved(x, T, dev, stream):
+    """(saved, address): x, or a new one."""
+    if x is None:
+        x = _new((T, 4), _F32, dev, stream)
+        return x, x.data_ptr()
+    return x, _operand(x, "saved", (T, 4), _F32, dev, False)[0]
+
+
 def _matrix(x, logits, dev, stream):
     """(dlogits, address, row stride): x, or a new matrix of the logits' shape and type."""
     if x is None:
         x = _new(logits.shape, logits.dtype, dev, stream)
+        return x, x.data_ptr(), x.shape[1]
     return (x, *_operand(x, "dlogits", logits.shape, logits.dtype, dev))
 
 
@@ -870,22 +909,20 @@ def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, save
     alternatives to list (0: none).  entropy=False leaves the entropy out (None).  saved: float32 [T, 4],
     what token_logprobs_grad reads (allocated where it is not given)."""
     dev, dt, T, V, px, ld = _logits(logits)
-    pt = _per_row(tokens, "tokens", T, torch.int32, dev)
+    pt = _per_row(tokens, "tokens", T, _I32, dev)
     st = _stream_on(stream, dev)
     logp = H = top = topl = pl = ph = ptop = ptl = None
     if pt is not None:
-        logp = _new((T,), torch.float32, dev, stream)
+        logp = _new((T,), _F32, dev, stream)
         pl = logp.data_ptr()
     if entropy:
-        H = _new((T,), torch.float32, dev, stream)
+        H = _new((T,), _F32, dev, stream)
         ph = H.data_ptr()
     if topk > 0:
-        top = _new((T, topk), torch.int32, dev, stream)
-        topl = _new((T, topk), torch.float32, dev, stream)
+        top = _new((T, topk), _I32, dev, stream)
+        topl = _new((T, topk), _F32, dev, stream)
         ptop, ptl = top.data_ptr(), topl.data_ptr()
-    if saved is None:
-        saved = _new((T, 4), torch.float32, dev, stream)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    saved, ps = _saved(saved, T, dev, stream)
     _check(lib().poet_token_logprobs(px, ld, dt, T, V, scale, pt, topk, pl, ph, ptop, ptl, ps, st))
     return logp, H, top, topl, saved
 
@@ -894,10 +931,10 @@ def token_logprobs_grad(logits, tokens, saved, dlogp=None, dentropy=None, *, sca
     """dlogits for the gradients dlogp and dentropy (float32 [T], either may be None) of token_logprobs's
     results; saved: the forward's.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
-    pt = _per_row(tokens, "tokens", T, torch.int32, dev)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
-    pl = _per_row(dlogp, "dlogp", T, torch.float32, dev)
-    pe = _per_row(dentropy, "dentropy", T, torch.float32, dev)
+    pt = _per_row(tokens, "tokens", T, _I32, dev)
+    ps = _operand(saved, "saved", (T, 4), _F32, dev, False)[0]
+    pl = _per_row(dlogp, "dlogp", T, _F32, dev)
+    pe = _per_row(dentropy, "dentropy", T, _F32, dev)
     st = _stream_on(stream, dev)
     dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
     _check(lib().poet_token_logprobs_grad(px, ld, dt, T, V, scale, pt, ps, pl, pe, pd, ldd, st))
@@ -908,8 +945,8 @@ def _teacher(teacher_tokens, teacher_values, T, dev):
     if teacher_tokens.dim() != 2:
         raise ValueError("teacher_tokens must be 2-D (tokens x entries)")
     K = teacher_tokens.shape[1]
-    return (_operand(teacher_tokens, "teacher_tokens", (T, K), torch.int32, dev, False)[0],
-            _operand(teacher_values, "teacher_values", (T, K), torch.float32, dev, False)[0], min(K, _MAXI32))
+    return (_operand(teacher_tokens, "teacher_tokens", (T, K), _I32, dev, False)[0],
+            _operand(teacher_values, "teacher_values", (T, K), _F32, dev, False)[0], min(K, _MAXI32))
 
 
 def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tail=False, scale=1.0, dloss=None,
@@ -922,12 +959,10 @@ def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tai
     float32 [T], None = 1), formed in the same pass; otherwise None.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
-    pw = _per_row(dloss, "dloss", T, torch.float32, dev)
+    pw = _per_row(dloss, "dloss", T, _F32, dev)
     st = _stream_on(stream, dev)
-    loss = _new((T,), torch.float32, dev, stream)
-    if saved is None:
-        saved = _new((T, 4), torch.float32, dev, stream)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    loss = _new((T,), _F32, dev, stream)
+    saved, ps = _saved(saved, T, dev, stream)
     pd, ldd = None, 0
     if grad or dlogits is not None:
         dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
@@ -941,8 +976,8 @@ def distill_topk_grad(logits, teacher_tokens, teacher_values, saved, dloss=None,
     """dlogits = the gradient of sum dloss * loss, from the forward's saved.  dlogits may be logits."""
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
-    pw = _per_row(dloss, "dloss", T, torch.float32, dev)
-    ps = _operand(saved, "saved", (T, 4), torch.float32, dev, False)[0]
+    pw = _per_row(dloss, "dloss", T, _F32, dev)
+    ps = _operand(saved, "saved", (T, 4), _F32, dev, False)[0]
     st = _stream_on(stream, dev)
     dlogits, pd, ldd = _matrix(dlogits, logits, dev, stream)
     _check(lib().poet_distill_topk_grad(px, ld, dt, T, V, scale, pt, pv, K, value_scale, 1 if tail else 0, ps, pw, pd,
