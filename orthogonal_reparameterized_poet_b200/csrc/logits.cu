@@ -33,7 +33,7 @@ constexpr int MAX_K = 128;
 constexpr int MAX_CLUSTER = 8;
 constexpr int SLICE = 262144;  // most columns of one CTA
 constexpr int NT = 256;        // threads of the element-wise gradients
-constexpr int CAND = 2048;     // candidates kept at once by the selection
+constexpr int CAND = 1536;     // candidates kept at once by the selection: 192 vectors of 8
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -1e30f;
 
@@ -331,7 +331,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
 // The ring's barriers and the exchange of the cluster's CTAs.
 struct Pipe {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-  uint64_t join, gather;     // the cluster's exchanges of a row
+  uint64_t join;             // the cluster's exchange of a row
   uint64_t tfull[2], tempty[2];  // the teacher's buffers
   float4 part[2][MAX_CLUSTER];
   float4 warp[2][8];
@@ -345,7 +345,6 @@ __device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, cg::clu
       bar_init(&P.empty[i], NW);
     }
     bar_init(&P.join, size);
-    bar_init(&P.gather, size);
     for (int i = 0; i < 2; ++i) {
       bar_init(&P.tfull[i], 1);
       bar_init(&P.tempty[i], NW);
@@ -523,29 +522,74 @@ __device__ __forceinline__ void add_ends(Run &r, float xh, float xt, float c) {
 
 // ------------------------------------------------------------------ selection of the largest
 
-// Shared memory of the selection.  The logits of a thread in one stage are a
-// group; keys holds every group's largest (group k * NW * 32 + thread of stage
+// A row's sums and where its slice's maxima are, handed from the warps that
+// compute to those that select.  The logits of a thread in one stage are a
+// group; the keys are the groups' largest (group k * NW * 32 + thread of stage
 // k), ends those of the elements before and behind the slice's vectors.
-struct Select {
-  unsigned long long cand[CAND];
-  unsigned long long best[MAX_K];
-  unsigned list[256];
-  unsigned counts[2][8];
-  unsigned n, m;
+struct Hand {
+  int64_t row;
+  Sums all;
+  float logs, floor;
   float ends[2];
 };
-
-// The sum of a count over the CTA; one barrier, buffers alternate.
+// Shared memory of the selection.
+constexpr int LIST = 256;
+struct Select {
+  uint64_t full[2], empty[2], gather[2];
+  Hand hand[2];
+  unsigned long long cand[CAND];
+  unsigned long long best[MAX_K];
+  unsigned list[LIST];
+  unsigned counts[2][4];
+  unsigned n, m;
+};
+constexpr int SELECT_BAR = 2;
+// Warps that select beside NW that compute.
 template <int NW>
-__device__ __forceinline__ unsigned cta_count(Select &S, unsigned v, int &flip) {
+constexpr int select_warps() { return NW == 8 ? 4 : 2; }
+
+template <int NS>
+__device__ __forceinline__ void select_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(SELECT_BAR), "n"(NS * 32) : "memory");
+}
+// The same; whether any thread brings true.
+template <int NS>
+__device__ __forceinline__ bool select_any(bool v) {
+  unsigned any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(unsigned(v)), "n"(SELECT_BAR), "n"(NS * 32)
+      : "memory");
+  return any != 0;
+}
+// The sum of a count over the selecting warps; one barrier, buffers alternate.
+template <int NS>
+__device__ __forceinline__ unsigned select_count(Select &S, unsigned v, int tid, int &flip) {
   v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) S.counts[flip][threadIdx.x >> 5] = v;
-  warps_sync<NW>();
+  if ((tid & 31) == 0) S.counts[flip][tid >> 5] = v;
+  select_sync<NS>();
   unsigned total = 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) total += S.counts[flip][w];
+  for (int w = 0; w < NS; ++w) total += S.counts[flip][w];
   flip ^= 1;
   return total;
+}
+// Where a lane's n items go in a list that `cell` counts; the whole warp.
+__device__ __forceinline__ unsigned place_of(unsigned n, unsigned *cell) {
+  const int lane = threadIdx.x & 31;
+  unsigned upto = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  unsigned base = 0;
+  if (lane == 31 && upto) base = atomicAdd(cell, upto);
+  return __shfl_sync(0xffffffffu, base, 31) + upto - n;
 }
 
 __device__ __forceinline__ unsigned long long order_of(float x, unsigned index) {
@@ -554,8 +598,8 @@ __device__ __forceinline__ unsigned long long order_of(float x, unsigned index) 
 
 // The K largest logits of a slice (equal ones: the lower index first), in
 // falling order, as order_of, to S.best, 0 where there are fewer; -inf is never
-// among them.  `floor`: the smallest of the threads' maxima, `top`: the slice's
-// largest logit; no NaN.
+// among them.  H.floor: the smallest of the computing threads' maxima; top: a
+// bound of all; no NaN.
 //
 // The K-th largest of the groups' maxima is a bound that at least K logits
 // reach and few others: one between it and the `most`-th largest is found by
@@ -564,25 +608,26 @@ __device__ __forceinline__ unsigned long long order_of(float x, unsigned index) 
 // crowded groups leave too many candidates, the exact bound is found by
 // bisection over the slice's elements.
 template <typename T, int NW>
-__device__ void select_largest(Select &S, const float *keys, const T *x, const Slice<T> &sl, int nst, unsigned K,
-                               float floor, float top) {
-  constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E;
-  const int tid = threadIdx.x;
+__device__ void select_largest(Select &S, const Hand &H, const float *keys, const T *x, const Slice<T> &sl, unsigned K,
+                               int tid) {
+  constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E, NS = select_warps<NW>(), NN = NS * 32;
   const T *body = x + sl.lo + sl.head;
+  const int groups = (sl.nv + SV - 1) / SV * G;
+  const float top = H.all.m;
   int flip = 0;
   const unsigned most = K + K / 2 < 32 ? 32 : K + K / 2;  // <= 192 < 256
   auto groups_at = [&](float b) {
     unsigned n = 0;
-    for (int k = 0; k < nst; ++k) n += keys[k * G + tid] >= b;
-    if (tid == 0) n += (S.ends[0] >= b) + (S.ends[1] >= b);
-    return cta_count<NW>(S, n, flip);
+#pragma unroll 4
+    for (int k = tid; k < groups; k += NN) n += keys[k] >= b;
+    if (tid == 0) n += (H.ends[0] >= b) + (H.ends[1] >= b);
+    return select_count<NS>(S, n, tid, flip);
   };
-  const uint32_t kmin = KEY_MASKED + 1;  // the lowest finite logit
-  uint32_t lo = kmin, hi = key_of(top) + 1;  // groups at lo > most (once tested), at hi none
+  uint32_t lo = KEY_MASKED + 1, hi = key_of(top) + 1;  // more than `most` groups reach lo (once tested), none hi
   if (tid == 0) { S.n = 0; S.m = 0; }
   bool crowded = false;
-  const bool many = floor > -INFINITY && unsigned(G) > most;
-  if (many) lo = max(lo, key_of(floor));  // every thread has a group there
+  const bool many = H.floor > -INFINITY && unsigned(G) > most;
+  if (many) lo = max(lo, key_of(H.floor));  // every computing thread has a group there
   if (many || groups_at(of_key(lo)) > most) {
     for (int step = 0;; ++step) {
       if (hi - lo <= 1) {
@@ -599,53 +644,73 @@ __device__ void select_largest(Select &S, const float *keys, const T *x, const S
       else if (n > most) lo = mid;
       else { lo = mid; break; }
     }
-  } else {
-    warps_sync<NW>();  // S.n, S.m
   }
+  select_sync<NS>();  // S.n, S.m
   const float bound = of_key(lo);
   unsigned n = 0;
   if (!crowded) {
-    for (int k = 0; k < nst; ++k)
-      if (keys[k * G + tid] >= bound) S.list[atomicAdd(&S.m, 1u)] = unsigned(k * G + tid);
-    if (tid < 2 && S.ends[tid] >= bound) S.list[atomicAdd(&S.m, 1u)] = unsigned(nst * G + tid);
-    warps_sync<NW>();
-    const unsigned items = S.m * U;
-    auto push = [&](float v, unsigned idx) {
-      if (v >= bound) {
-        const unsigned at = atomicAdd(&S.n, 1u);
-        if (at < CAND) S.cand[at] = order_of(v, idx);
-      }
-    };
-    for (unsigned j = tid; j < items; j += G) {
-      const int g = int(S.list[j / U]), u = int(j % U);
-      if (g >= nst * G) {  // the ends
-        const int a = g == nst * G ? sl.lo : sl.tail0, b = g == nst * G ? sl.lo + sl.head : sl.hi;
-        for (int i = a + u; i < b; i += U) push(to_float(x[i]), unsigned(i));
-      } else {
-        const int v = g / G * SV + u * G + g % G;
-        if (v < sl.nv) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(body + int64_t(v) * E);
-          float2 f[E / 2];
-          Vec<T>::get(w, f);
+    unsigned mine = 0;
+#pragma unroll 4
+    for (int k = tid; k < groups; k += NN) mine += keys[k] >= bound;
+    unsigned at = place_of(mine, &S.m);
+    if (mine)
+      for (int k = tid; k < groups; k += NN)
+        if (keys[k] >= bound && at < LIST) S.list[at++] = unsigned(k);
+    select_sync<NS>();
+    const unsigned items = min(S.m, unsigned(LIST)) * U;
+    constexpr int AHEAD = 2;  // vectors that a thread reads at once
+    for (unsigned j0 = 0; j0 < items; j0 += AHEAD * NN) {
+      uint4 w[AHEAD];
+      int from[AHEAD];
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            push(f[i].x, unsigned(sl.lo + sl.head + v * E + 2 * i));
-            push(f[i].y, unsigned(sl.lo + sl.head + v * E + 2 * i + 1));
+      for (int q = 0; q < AHEAD; ++q) {
+        constexpr uint32_t M = Vec<T>::MASKED;
+        const unsigned j = j0 + q * NN + tid;
+        w[q] = make_uint4(M, M, M, M);
+        from[q] = 0;
+        if (j < items) {
+          const int g = int(S.list[j / U]), v = g / G * SV + int(j % U) * G + g % G;
+          if (v < sl.nv) {
+            w[q] = *reinterpret_cast<const uint4 *>(body + int64_t(v) * E);
+            from[q] = sl.lo + sl.head + v * E;
           }
         }
       }
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        float2 f[E / 2];
+        Vec<T>::get(w[q], f);
+        unsigned bits = 0;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) bits |= unsigned(f[i].x >= bound) << (2 * i) | unsigned(f[i].y >= bound) << (2 * i + 1);
+        unsigned to = place_of(__popc(bits), &S.n);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (bits >> i & 1u) {
+            if (to < CAND) S.cand[to] = order_of(i & 1 ? f[i / 2].y : f[i / 2].x, unsigned(from[q] + i));
+            ++to;
+          }
+      }
     }
-    warps_sync<NW>();
+    if (tid < 32) {  // the ends
+      const int ih = sl.lo + tid, it = sl.tail0 + tid;
+      const float xh = tid < sl.head ? to_float(x[ih]) : -INFINITY, xt = it < sl.hi ? to_float(x[it]) : -INFINITY;
+      unsigned to = place_of(unsigned(xh >= bound) + unsigned(xt >= bound), &S.n);
+      if (xh >= bound && to < CAND) S.cand[to] = order_of(xh, unsigned(ih));
+      to += xh >= bound;
+      if (xt >= bound && to < CAND) S.cand[to] = order_of(xt, unsigned(it));
+    }
+    select_sync<NS>();
     n = S.n;
   }
   if (crowded || n > CAND) {
     // the exact bound: the largest that K elements reach (elements of groups below it need not be read), then,
     // among the elements equal to it, the index that leaves K
     auto each = [&](float from, auto &&f) {
-      for (int k = 0; k < nst; ++k)
-        if (keys[k * G + tid] >= from)
+      for (int k = tid; k < groups; k += NN)
+        if (keys[k] >= from)
           for (int u = 0; u < U; ++u) {
-            const int v = k * SV + u * G + tid;
+            const int v = k / G * SV + u * G + k % G;
             if (v < sl.nv)
               for (int i = 0; i < E; ++i) f(to_float(body[int64_t(v) * E + i]), sl.lo + sl.head + v * E + i);
           }
@@ -657,7 +722,7 @@ __device__ void select_largest(Select &S, const float *keys, const T *x, const S
     auto elements_at = [&](float b) {
       unsigned c = 0;
       each(b, [&](float v, int) { c += v >= b; });
-      return cta_count<NW>(S, c, flip);
+      return select_count<NS>(S, c, tid, flip);
     };
     uint32_t l = lo, h = key_of(top) + 1;  // at least K reach l, none h
     while (h - l > 1) {
@@ -668,24 +733,24 @@ __device__ void select_largest(Select &S, const float *keys, const T *x, const S
     const float b = of_key(l);
     unsigned c = 0;
     each(b, [&](float v, int) { c += v > b; });
-    const unsigned left = K - cta_count<NW>(S, c, flip);
+    const unsigned left = K - select_count<NS>(S, c, tid, flip);
     int il = sl.lo, ih = sl.hi;  // fewer than `left` equal ones before il, at least `left` before ih
     while (ih - il > 1) {
       const int mid = il + (ih - il) / 2;
       c = 0;
       each(b, [&](float v, int i) { c += v == b && i < mid; });
-      if (cta_count<NW>(S, c, flip) >= left) ih = mid;
+      if (select_count<NS>(S, c, tid, flip) >= left) ih = mid;
       else il = mid;
     }
     if (tid == 0) S.n = 0;
-    warps_sync<NW>();
+    select_sync<NS>();
     each(b, [&](float v, int i) {
       if (v > b || (v == b && i < ih)) {
         const unsigned at = atomicAdd(&S.n, 1u);
         if (at < CAND) S.cand[at] = order_of(v, unsigned(i));
       }
     });
-    warps_sync<NW>();
+    select_sync<NS>();
     n = min(S.n, unsigned(CAND));
   } else if (n > 2 * most) {
     // many in the listed groups: a closer bound among the candidates (their order has no ties)
@@ -693,36 +758,32 @@ __device__ void select_largest(Select &S, const float *keys, const T *x, const S
     while (h - l > 1) {
       const unsigned long long mid = l + (h - l) / 2;
       unsigned c = 0;
-      for (unsigned i = tid; i < n; i += G) c += S.cand[i] >= mid;
-      c = cta_count<NW>(S, c, flip);
+      for (unsigned i = tid; i < n; i += NN) c += S.cand[i] >= mid;
+      c = select_count<NS>(S, c, tid, flip);
       if (c < K) h = mid;
       else if (c > most) l = mid;
       else { l = mid; break; }
     }
-    unsigned long long mine[CAND / G];
-#pragma unroll
-    for (int i = 0; i < CAND / G; ++i) {
-      const unsigned j = tid + i * G;
-      mine[i] = j < n && S.cand[j] >= l ? S.cand[j] : 0;
-    }
     if (tid == 0) S.n = 0;
-    warps_sync<NW>();
-#pragma unroll
-    for (int i = 0; i < CAND / G; ++i)
-      if (mine[i]) S.cand[atomicAdd(&S.n, 1u)] = mine[i];
-    warps_sync<NW>();
+    for (unsigned i0 = 0; i0 < n; i0 += NN) {  // those that reach it move to the front: never past what is read
+      const unsigned i = i0 + tid;
+      const unsigned long long mine = i < n ? S.cand[i] : 0;
+      select_sync<NS>();
+      if (i < n && mine >= l) S.cand[atomicAdd(&S.n, 1u)] = mine;
+    }
+    select_sync<NS>();
     n = S.n;
   }
-  for (unsigned i = tid; i < K; i += G)
+  for (unsigned i = tid; i < K; i += NN)
     if (i >= n) S.best[i] = 0;
-  for (unsigned i = tid; i < n; i += G) {
+  for (unsigned i = tid; i < n; i += NN) {
     const unsigned long long mine = S.cand[i];
     unsigned above = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (unsigned j = 0; j < n; ++j) above += S.cand[j] > mine;
     if (above < K) S.best[above] = mine;
   }
-  warps_sync<NW>();
+  select_sync<NS>();
 }
 
 // ------------------------------------------------------------------ log probabilities
@@ -731,6 +792,7 @@ struct LogpArgs {
   const void *x;
   int64_t ld, T;
   int V, K, stages;
+  int key_floats;  // of one of the two buffers of keys
   float scale;
   const int32_t *tokens;
   float *logp, *entropy, *top_logp, *saved;
@@ -747,16 +809,14 @@ struct GivenTokens {
 
 // The computing warps' part.
 template <typename T, int NW, bool TOP, bool ENT>
-__device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, unsigned char *ring, int rank, int size,
-                                          int64_t first, int64_t step) {
+__device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S, float *keys0, const unsigned char *ring,
+                                          int rank, int size, int64_t first, int64_t step) {
   constexpr int G = NW * 32, SV = G * U;
   const int tid = threadIdx.x;
-  Select &S = *reinterpret_cast<Select *>(ring + a.stages * (SV * 16));
-  unsigned long long *gather = reinterpret_cast<unsigned long long *>(&S + 1);  // [size][K], the first CTA's
-  float *keys = reinterpret_cast<float *>(gather + (size > 1 ? size * a.K : 0));
   const float c = a.scale * LOG2E;
   Spot at;
-  int par = 0, gathered = 0;
+  int par = 0;
+  uint32_t round = 0;  // rows handed to the selection
   int token = a.tokens && first < a.T ? a.tokens[first] : -1;
   for (int64_t row = first; row < a.T; row += step) {
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
@@ -788,6 +848,9 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, unsigned c
       if (tid < sl.head) xh = to_float(x[sl.lo + tid]);
       if (sl.tail0 + tid < sl.hi) xt = to_float(x[sl.tail0 + tid]);
     }
+    const int buf = int(round & 1);
+    float *keys = keys0 + buf * a.key_floats;
+    if (TOP) bar_wait(&S.empty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
     for (int k = 0; k < nst; ++k) {
       uint4 v[U];
       bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
@@ -804,94 +867,156 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, unsigned c
       if (TOP) {
         const uint32_t kh = __reduce_max_sync(0xffffffffu, key_of(xh)), kt = __reduce_max_sync(0xffffffffu, key_of(xt));
         if (tid == 0) {
-          S.ends[0] = of_key(kh);
-          S.ends[1] = of_key(kt);
+          S.hand[buf].ends[0] = of_key(kh);
+          S.hand[buf].ends[1] = of_key(kt);
         }
       }
     }
-    const Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, TOP ? &floor : nullptr, !TOP && size == 1);
+    const Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, TOP ? &floor : nullptr, size == 1);
     par ^= 1;
-    if (!TOP && size == 1 && tid >= 32) continue;
-    const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
-    const float logs = logf(all.s);        // -inf for a row of masks
-    if (rank == 0 && tid == 0) {
-      float H = 0.f;
-      if (bad) H = NAN;
-      else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
-      if (a.logp) a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
-      if (a.entropy) a.entropy[row] = H;
-      if (a.saved)
-        reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
-    }
-    if (!TOP) continue;
-    const unsigned K = unsigned(a.K);
-    if (bad) {
-      if (rank == 0)
-        for (unsigned k = tid; k < K; k += G) {
-          a.top_tokens[row * K + k] = -1;
-          a.top_logp[row * K + k] = NAN;
+    if (tid < 32) {
+      const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
+      const float logs = logf(all.s);        // -inf for a row of masks
+      if (tid == 0) {
+        float H = 0.f;
+        if (bad) H = NAN;
+        else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
+        if (rank == 0) {
+          if (a.logp) a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
+          if (a.entropy) a.entropy[row] = H;
+          if (a.saved)
+            reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
         }
-      continue;
-    }
-    auto put = [&](unsigned k, unsigned long long b) {
-      a.top_tokens[row * K + k] = b ? int32_t(0xffffffffu - uint32_t(b)) : -1;
-      a.top_logp[row * K + k] = b ? (of_key(uint32_t(b >> 32)) - all.m) * a.scale - logs : -INFINITY;
-    };
-    select_largest<T, NW>(S, keys, x, sl, nst, K, floor, all.m);
-    if (size == 1) {
-      for (unsigned k = tid; k < K; k += G) put(k, S.best[k]);
-      warps_sync<NW>();  // S is written again in the next row
-      continue;
-    }
-    // the CTAs' lists to the first one, which merges them: an element's place is its place in its list plus the
-    // numbers of larger elements in the others
-    for (unsigned k = tid; k < K; k += G)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_at(smem_at(gather + rank * K + k), 0)), "l"(S.best[k])
-                   : "memory");
-    warps_sync<NW>();
-    if (tid == 0) bar_arrive_peer(&P.gather, 0);
-    if (rank != 0) continue;
-    bar_wait(&P.gather, gathered, &P.abort, a.errword);
-    gathered ^= 1;
-    unsigned found = 0;
-    for (unsigned i = tid; i < size * K; i += G) {
-      const unsigned long long mine = gather[i];
-      if (!mine) continue;
-      ++found;
-      unsigned place = i % K;
-      for (int q = 0; q < size; ++q) {
-        if (q == int(i / K)) continue;
-        unsigned l = 0, h = K;  // the first place of list q that is not larger
-        while (l < h) {
-          const unsigned mid = (l + h) / 2;
-          if (gather[q * K + mid] > mine) l = mid + 1;
-          else h = mid;
+        if (TOP) {
+          Hand &h = S.hand[buf];
+          h.row = row;
+          h.all = all;
+          h.logs = logs;
+          h.floor = floor;
         }
-        place += l;
       }
-      if (place < K) put(place, mine);
     }
-    int flip = 0;
-    found = cta_count<NW>(S, found, flip);
-    for (unsigned k = found + tid; k < K; k += G) put(k, 0);
-    warps_sync<NW>();
+    if (TOP) {
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(&S.full[buf]);
+      ++round;
+    }
+  }
+  if (TOP) {  // no more rows
+    const int buf = int(round & 1);
+    bar_wait(&S.empty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
+    if (tid == 0) S.hand[buf].row = -1;
+    __syncwarp();
+    if ((tid & 31) == 0) bar_arrive(&S.full[buf]);
   }
 }
 
-// NW warps compute, one more streams the rows.
+// The selecting warps' part: the alternatives of the rows behind the one that is
+// being summed.
+template <typename T, int NW>
+__device__ __forceinline__ void select_rows(const LogpArgs &a, Pipe &P, Select &S, const float *keys0,
+                                            unsigned long long *gather0, int rank, int size, int tid) {
+  constexpr int NS = select_warps<NW>(), NN = NS * 32;
+  const unsigned K = unsigned(a.K);
+  for (uint32_t round = 0;; ++round) {
+    const int buf = int(round & 1);
+    const uint32_t phase = round >> 1 & 1;
+    // all leave together: a warp that stayed would wait for the others
+    if (select_any<NS>(!bar_wait(&S.full[buf], phase, &P.abort, a.errword))) break;
+    const Hand &h = S.hand[buf];
+    const int64_t row = h.row;
+    if (row < 0) break;
+    const bool bad = !(h.all.s < INFINITY);
+    auto release = [&]() {
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(&S.empty[buf]);
+    };
+    auto put = [&](unsigned k, unsigned long long b) {
+      a.top_tokens[row * K + k] = b ? int32_t(0xffffffffu - uint32_t(b)) : -1;
+      a.top_logp[row * K + k] = bad ? NAN : b ? (of_key(uint32_t(b >> 32)) - h.all.m) * a.scale - h.logs : -INFINITY;
+    };
+    if (bad) {
+      for (unsigned k = tid; k < K; k += NN) S.best[k] = 0;
+      select_sync<NS>();
+    } else {
+      const T *x = static_cast<const T *>(a.x) + row * a.ld;
+      select_largest<T, NW>(S, h, keys0 + buf * a.key_floats, x, slice_of(x, a.V, rank, size), K, tid);
+    }
+    if (size == 1) {
+      for (unsigned k = tid; k < K; k += NN) put(k, S.best[k]);
+      release();
+      select_sync<NS>();  // S.best is written again in the next row
+      continue;
+    }
+    // the CTAs' lists to the first one, which merges them: an element's place is its place in its list plus the
+    // numbers of larger elements in the others.  Two buffers: the others are at most one row ahead of the first.
+    unsigned long long *gather = gather0 + buf * size * K;
+    for (unsigned k = tid; k < K; k += NN)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_at(smem_at(gather + rank * K + k), 0)), "l"(S.best[k])
+                   : "memory");
+    select_sync<NS>();
+    if (tid == 0) bar_arrive_peer(&S.gather[buf], 0);
+    if (rank == 0) {
+      bar_wait(&S.gather[buf], phase, &P.abort, a.errword);
+      unsigned found = 0;
+      for (unsigned i = tid; i < size * K; i += NN) {
+        const unsigned long long mine = gather[i];
+        if (!mine) continue;
+        ++found;
+        unsigned place = i % K;
+        for (int q = 0; q < size; ++q) {
+          if (q == int(i / K)) continue;
+          unsigned l = 0, hi = K;  // the first place of list q that is not larger
+          while (l < hi) {
+            const unsigned mid = (l + hi) / 2;
+            if (gather[q * K + mid] > mine) l = mid + 1;
+            else hi = mid;
+          }
+          place += l;
+        }
+        if (place < K) put(place, mine);
+      }
+      int flip = 0;
+      found = select_count<NS>(S, found, tid, flip);
+      for (unsigned k = found + tid; k < K; k += NN) put(k, 0);
+    }
+    release();
+    select_sync<NS>();
+  }
+}
+
+template <int NW, bool TOP>
+constexpr int logp_threads() { return (NW + 1 + (TOP ? select_warps<NW>() : 0)) * 32; }
+
+// NW warps compute, one more streams the rows, and where alternatives are wanted
+// a few select them, a row behind: a selection is a chain of short steps, which
+// the next row's sums hide.
 template <typename T, int NW, bool TOP, bool ENT>
-__global__ void __launch_bounds__((NW + 1) * 32, per_sm<NW>(!TOP)) logp_kernel(const LogpArgs a) {
+__global__ void __launch_bounds__(logp_threads<NW, TOP>(), per_sm<NW>(!TOP)) logp_kernel(const LogpArgs a) {
+  constexpr int G = NW * 32;
   __shared__ Pipe P;
   extern __shared__ __align__(128) unsigned char ring[];
   cg::cluster_group cl = cg::this_cluster();
   const int size = int(cl.num_blocks()), rank = int(cl.block_rank());
   const int64_t first = blockIdx.x / size, step = gridDim.x / size;
+  const int tid = threadIdx.x;
+  Select &S = *reinterpret_cast<Select *>(ring + a.stages * (G * U * 16));
+  unsigned long long *gather = reinterpret_cast<unsigned long long *>(&S + 1);  // [2][size][K], the first CTA's
+  float *keys = reinterpret_cast<float *>(gather + (size > 1 ? 2 * size * a.K : 0));
+  if (TOP && tid == 0)
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&S.full[i], NW);
+      bar_init(&S.empty[i], select_warps<NW>());
+      bar_init(&S.gather[i], size);
+    }
   pipe_init<NW>(P, a.stages, size, cl);
-  if (threadIdx.x >= NW * 32)
+  if (tid < G)
+    logp_rows<T, NW, TOP, ENT>(a, P, S, keys, ring, rank, size, first, step);
+  else if (tid < G + 32)
     produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, false, a.errword,
                    GivenTokens{a.tokens, a.V, 0});
-  else
-    logp_rows<T, NW, TOP, ENT>(a, P, ring, rank, size, first, step);
+  else if (TOP)
+    select_rows<T, NW>(a, P, S, keys, gather, rank, size, tid - G - 32);
   if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
@@ -1533,20 +1658,21 @@ poet_status check_out(const char *what, const void *x, int64_t ld, const void *o
 bool al(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // How the rows are spread: CTAs of NW computing warps, clusters of `cluster` of
-// them, and the stages that fit beside `extra` bytes where `per_sm` CTAs share an SM.
+// them, and the stages that fit beside `extra` bytes (and the `fixed` ones of the
+// kernel's static shared memory and the system) where `per_sm` CTAs share an SM.
 struct Spread {
   int cluster, stages;
   unsigned grid;
   size_t smem;
 };
 template <int NW>
-Spread spread(int64_t rows, int cluster, size_t extra, int per_sm) {
-  constexpr size_t STAGE = size_t(NW) * 32 * U * 16, STATIC = 10 * 1024, SM = 228 * 1024;
+Spread spread(int64_t rows, int cluster, size_t extra, size_t fixed, int per_sm) {
+  constexpr size_t STAGE = size_t(NW) * 32 * U * 16, SM = 228 * 1024;
   Spread s;
   s.cluster = cluster;
   size_t left = 0;
   for (;; --per_sm) {  // at least four stages, or two of one CTA alone
-    left = std::min<size_t>(SM / per_sm - STATIC, 227 * 1024 - STATIC);
+    left = std::min<size_t>(SM / per_sm, 227 * 1024) - fixed;
     if (left >= extra + 4 * STAGE || per_sm == 1) break;
   }
   s.stages = int(std::min<size_t>((left - extra) / STAGE, MAX_STAGES));
@@ -1580,19 +1706,18 @@ constexpr int NARROW = 8192;
 
 template <typename T, int NW>
 poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
-  constexpr int THREADS = (NW + 1) * 32;
   const int64_t nv = a.V / Vec<T>::E / cluster + 1, nst = (nv + NW * 32 * U - 1) / (NW * 32 * U);
+  a.key_floats = int(nst) * NW * 32;
   size_t extra = 0;
-  if (a.K)
-    extra = sizeof(Select) + (cluster > 1 ? size_t(cluster) * a.K * 8 : 0) + size_t(nst) * NW * 32 * 4;
-  const Spread s = spread<NW>(a.T, cluster, extra, per_sm<NW>(!a.K));
+  if (a.K) extra = sizeof(Select) + (cluster > 1 ? size_t(2) * cluster * a.K * 8 : 0) + size_t(2) * a.key_floats * 4;
+  const Spread s = spread<NW>(a.T, cluster, extra, 2048, per_sm<NW>(!a.K));
   a.stages = s.stages;
   const bool ent = a.entropy || a.saved;
   if (a.K)
-    return ent ? launch_rows<logp_kernel<T, NW, true, true>>(a, s, THREADS, st, "logprobs")
-               : launch_rows<logp_kernel<T, NW, true, false>>(a, s, THREADS, st, "logprobs");
-  return ent ? launch_rows<logp_kernel<T, NW, false, true>>(a, s, THREADS, st, "logprobs")
-             : launch_rows<logp_kernel<T, NW, false, false>>(a, s, THREADS, st, "logprobs");
+    return ent ? launch_rows<logp_kernel<T, NW, true, true>>(a, s, logp_threads<NW, true>(), st, "logprobs")
+               : launch_rows<logp_kernel<T, NW, true, false>>(a, s, logp_threads<NW, true>(), st, "logprobs");
+  return ent ? launch_rows<logp_kernel<T, NW, false, true>>(a, s, logp_threads<NW, false>(), st, "logprobs")
+             : launch_rows<logp_kernel<T, NW, false, false>>(a, s, logp_threads<NW, false>(), st, "logprobs");
 }
 template <typename T>
 poet_status run_logp(LogpArgs &a, cudaStream_t st) {
@@ -1604,7 +1729,7 @@ template <typename T, int NW>
 poet_status run_distill(DistillArgs &a, int cluster, cudaStream_t st) {
   constexpr int THREADS = (NW + 3) * 32;
   const size_t marks = a.tail ? mark_bytes_of<T>(a.V, cluster) : 0;
-  const Spread s = spread<NW>(a.T, cluster, 2 * marks, per_sm<NW>(false));
+  const Spread s = spread<NW>(a.T, cluster, 2 * marks, 11 * 1024, per_sm<NW>(false));
   a.stages = s.stages;
   return a.out ? launch_rows<distill_kernel<T, NW, true>>(a, s, THREADS, st, "distill")
                : launch_rows<distill_kernel<T, NW, false>>(a, s, THREADS, st, "distill");
