@@ -332,13 +332,14 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
 struct Pipe {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t join;             // the cluster's exchange of a row
-  uint64_t tfull[2], tempty[2];  // the teacher's buffers
+  uint64_t hfull[2], hempty[2];  // two buffers handed from some warps to others
   float4 part[2][MAX_CLUSTER];
   float4 warp[2][8];
   int abort;
 };
+// from, to: warps that fill a buffer and that empty it.
 template <int NW>
-__device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, cg::cluster_group &cl) {
+__device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, int from, int to, cg::cluster_group &cl) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       bar_init(&P.full[i], 1);
@@ -346,8 +347,8 @@ __device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, cg::clu
     }
     bar_init(&P.join, size);
     for (int i = 0; i < 2; ++i) {
-      bar_init(&P.tfull[i], 1);
-      bar_init(&P.tempty[i], NW);
+      bar_init(&P.hfull[i], from);
+      bar_init(&P.hempty[i], to);
     }
     P.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -472,42 +473,39 @@ __device__ __forceinline__ float add_vectors(Run &r, const uint4 (&v)[U], float 
   return mx;
 }
 
-// Joins the threads' sums of a row: all threads of the CTA (and of the cluster)
-// get the row's sums.  `par` is the row's parity among those that this CTA
-// joins: the buffers alternate, and a buffer is written again only after the
-// barrier (the exchange) of the row between.  *floor: a value of each thread's;
-// the CTA's smallest on return.
+// A row's sums from those of the NW warps in P.warp[par], and of the cluster's
+// CTAs: by whole warps, of which `leads` says which exchanges with the others.
+// The buffers of the exchange alternate with `par`: one is written again only
+// after the exchange of the row between, for which each CTA's leading warp
+// arrives after all its warps have read the first.
 template <int NW>
-__device__ __forceinline__ Sums join_row(Pipe &P, Run &r, float c, int par, int rank, int size, unsigned *errword,
-                                         float *floor, bool one_warp = false) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float low = floor ? of_key(__reduce_min_sync(0xffffffffu, key_of(*floor))) : 0.f;
-  const Sums w = join_warp(r, c);
-  if (lane == 0) P.warp[par][warp] = make_float4(w.m, w.s, w.t, low);
-  warps_sync<NW>();
-  if (one_warp && warp != 0) return {0.f, 0.f, 0.f};
+__device__ __forceinline__ Sums join_warps(Pipe &P, float c, int par, int phase, bool leads, int rank, int size,
+                                           unsigned *errword) {
+  const int lane = threadIdx.x & 31;
   const float4 f = P.warp[par][lane % NW];
   Sums all = join_lanes<NW == 8 ? 3 : 1>({f.x, f.y, f.z}, c);
-  if (floor) {
-    float m = f.w;
-#pragma unroll
-    for (int o = NW / 2; o > 0; o >>= 1) m = fminf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    *floor = m;
-  }
   if (size > 1) {
-    if (warp == 0 && lane < size) {
+    if (leads && lane < size) {
       const uint32_t to = peer_at(smem_at(&P.part[par][rank]), lane);
       asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(all.m), "f"(all.s), "f"(all.t),
                    "f"(0.f)
                    : "memory");
       bar_arrive_peer(&P.join, lane);
     }
-    bar_wait(&P.join, par, &P.abort, errword);
+    bar_wait(&P.join, phase, &P.abort, errword);
     const int q = lane % MAX_CLUSTER;
     const float4 g = q < size ? P.part[par][q] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
     all = join_lanes<3>({g.x, g.y, g.z}, c);
   }
   return all;
+}
+// The same with the warps that compute, all of whose threads get the sums.
+template <int NW>
+__device__ __forceinline__ Sums join_row(Pipe &P, Run &r, float c, int par, int rank, int size, unsigned *errword) {
+  const Sums w = join_warp(r, c);
+  if ((threadIdx.x & 31) == 0) P.warp[par][threadIdx.x >> 5] = make_float4(w.m, w.s, w.t, 0.f);
+  warps_sync<NW>();
+  return join_warps<NW>(P, c, par, par, threadIdx.x < 32, rank, size, errword);
 }
 
 // The ragged ends of a slice, at most E - 1 elements each, one per lane of the
@@ -522,24 +520,23 @@ __device__ __forceinline__ void add_ends(Run &r, float xh, float xt, float c) {
 
 // ------------------------------------------------------------------ selection of the largest
 
-// A row's sums and where its slice's maxima are, handed from the warps that
-// compute to those that select.  The logits of a thread in one stage are a
+// Where a slice's largest logits are.  The logits of a thread in one stage are a
 // group; the keys are the groups' largest (group k * NW * 32 + thread of stage
-// k), ends those of the elements before and behind the slice's vectors.
+// k), tops the computing threads', ends those of the elements before and behind
+// the slice's vectors.
 struct Hand {
-  int64_t row;
-  Sums all;
-  float logs, floor;
   float ends[2];
+  float tops[256];
 };
 // Shared memory of the selection.
 constexpr int LIST = 256;
+constexpr unsigned MOST = 192;  // groups that are listed
 struct Select {
-  uint64_t full[2], empty[2], gather[2];
+  uint64_t gather[2];
   Hand hand[2];
   unsigned long long cand[CAND];
   unsigned long long best[MAX_K];
-  unsigned list[LIST];
+  unsigned short list[LIST];  // of fewer than 2^16 groups: SLICE / (4 U) and a stage
   unsigned counts[2][4];
   unsigned n, m;
 };
@@ -598,22 +595,22 @@ __device__ __forceinline__ unsigned long long order_of(float x, unsigned index) 
 
 // The K largest logits of a slice (equal ones: the lower index first), in
 // falling order, as order_of, to S.best, 0 where there are fewer; -inf is never
-// among them.  H.floor: the smallest of the computing threads' maxima; top: a
-// bound of all; no NaN.
+// among them.  floor: the smallest of the computing threads' maxima; top: no
+// logit is larger; no NaN.
 //
-// The K-th largest of the groups' maxima is a bound that at least K logits
-// reach and few others: one between it and the `most`-th largest is found by
-// bisection, first of values, then of the order of floats; then only the
-// groups that reach it are read again (from L2).  Where equal logits or a few
-// crowded groups leave too many candidates, the exact bound is found by
-// bisection over the slice's elements.
+// The K-th largest of some maxima of disjoint parts is a bound that at least K
+// logits reach and few others.  The parts are first the computing threads'
+// logits (G values, found about by bisection); only the groups that reach that
+// bound are read again (from L2).  Where more than MOST groups do, the bound is
+// drawn closer with the groups' maxima; where equal logits or a few crowded
+// groups leave too many candidates, the exact bound is found by bisection over
+// the slice's elements.
 template <typename T, int NW>
 __device__ void select_largest(Select &S, const Hand &H, const float *keys, const T *x, const Slice<T> &sl, unsigned K,
-                               int tid) {
+                               float floor, float top, int tid) {
   constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E, NS = select_warps<NW>(), NN = NS * 32;
   const T *body = x + sl.lo + sl.head;
   const int groups = (sl.nv + SV - 1) / SV * G;
-  const float top = H.all.m;
   int flip = 0;
   const unsigned most = K + K / 2 < 32 ? 32 : K + K / 2;  // <= 192 < 256
   auto groups_at = [&](float b) {
@@ -623,39 +620,71 @@ __device__ void select_largest(Select &S, const Hand &H, const float *keys, cons
     if (tid == 0) n += (H.ends[0] >= b) + (H.ends[1] >= b);
     return select_count<NS>(S, n, tid, flip);
   };
-  uint32_t lo = KEY_MASKED + 1, hi = key_of(top) + 1;  // more than `most` groups reach lo (once tested), none hi
+  uint32_t lo = KEY_MASKED + 1, hi = key_of(top) + 1;  // none reach hi
+  // A value between lo and hi, of values for some steps, then of the order of floats.
+  auto between = [&](int step) {
+    const float v = 0.5f * of_key(lo) + 0.5f * of_key(hi - 1);
+    return step < 12 ? min(max(key_of(v), lo + 1), hi - 1) : lo + (hi - lo) / 2;
+  };
   if (tid == 0) { S.n = 0; S.m = 0; }
+  select_sync<NS>();
+  if (K <= unsigned(G) && floor > -INFINITY) {
+    // every computing thread has logits: the K-th largest of their maxima first
+    float t[G / NN];
+#pragma unroll
+    for (int i = 0; i < G / NN; ++i) t[i] = H.tops[tid + i * NN];
+    lo = max(lo, key_of(floor));
+    for (int step = 0; hi - lo > 1; ++step) {
+      const uint32_t mid = between(step);
+      unsigned n = 0;
+#pragma unroll
+      for (int i = 0; i < G / NN; ++i) n += t[i] >= of_key(mid);
+      n = select_count<NS>(S, n, tid, flip);
+      if (n < K) hi = mid;
+      else {
+        lo = mid;
+        if (n <= K + K / 8 + 2) break;
+      }
+    }
+    hi = key_of(top) + 1;
+  }
+  // the groups that reach the bound
+  unsigned mine = 0, at = 0;
   bool crowded = false;
-  const bool many = H.floor > -INFINITY && unsigned(G) > most;
-  if (many) lo = max(lo, key_of(H.floor));  // every computing thread has a group there
-  if (many || groups_at(of_key(lo)) > most) {
+  auto count_mine = [&]() {
+    mine = 0;
+#pragma unroll 4
+    for (int k = tid; k < groups; k += NN) mine += keys[k] >= of_key(lo);
+    at = place_of(mine, &S.m);
+    select_sync<NS>();
+  };
+  count_mine();
+  if (S.m + 2 > MOST) {  // a closer one: at least K reach it, no more than `most`
     for (int step = 0;; ++step) {
       if (hi - lo <= 1) {
         crowded = true;
         break;
       }
-      uint32_t mid = lo + (hi - lo) / 2;
-      if (step < 12) {
-        const float v = 0.5f * of_key(lo) + 0.5f * of_key(hi - 1);
-        mid = min(max(key_of(v), lo + 1), hi - 1);
-      }
+      const uint32_t mid = between(step);
       const unsigned n = groups_at(of_key(mid));
       if (n < K) hi = mid;
-      else if (n > most) lo = mid;
-      else { lo = mid; break; }
+      else {
+        lo = mid;
+        if (n <= most) break;
+      }
+    }
+    if (!crowded) {
+      if (tid == 0) S.m = 0;
+      select_sync<NS>();
+      count_mine();
     }
   }
-  select_sync<NS>();  // S.n, S.m
   const float bound = of_key(lo);
   unsigned n = 0;
   if (!crowded) {
-    unsigned mine = 0;
-#pragma unroll 4
-    for (int k = tid; k < groups; k += NN) mine += keys[k] >= bound;
-    unsigned at = place_of(mine, &S.m);
     if (mine)
       for (int k = tid; k < groups; k += NN)
-        if (keys[k] >= bound && at < LIST) S.list[at++] = unsigned(k);
+        if (keys[k] >= bound && at < LIST) S.list[at++] = (unsigned short)k;
     select_sync<NS>();
     const unsigned items = min(S.m, unsigned(LIST)) * U;
     constexpr int AHEAD = 2;  // vectors that a thread reads at once
@@ -807,7 +836,8 @@ struct GivenTokens {
   __device__ __forceinline__ bool live() const { return token >= 0 && token < V; }
 };
 
-// The computing warps' part.
+// The computing warps' part: each warp's sums of every row, and what the
+// selection needs.  They never wait for one another.
 template <typename T, int NW, bool TOP, bool ENT>
 __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S, float *keys0, const unsigned char *ring,
                                           int rank, int size, int64_t first, int64_t step) {
@@ -815,30 +845,13 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
   const int tid = threadIdx.x;
   const float c = a.scale * LOG2E;
   Spot at;
-  int par = 0;
-  uint32_t round = 0;  // rows handed to the selection
-  int token = a.tokens && first < a.T ? a.tokens[first] : -1;
+  uint32_t round = 0;  // rows handed over
+  int token = a.tokens && first < a.T ? a.tokens[first] : 0;
   for (int64_t row = first; row < a.T; row += step) {
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
     const int y = token;
     if (a.tokens && row + step < a.T) token = a.tokens[row + step];
-    if (a.tokens && (y < 0 || y >= a.V)) {  // the whole cluster takes this way
-      if (rank != 0) continue;
-      if (tid == 0) {
-        if (y >= a.V) atomicOr(a.errword, unsigned(ERR_BOUNDS));
-        if (a.logp) a.logp[row] = 0.f;
-        if (a.entropy) a.entropy[row] = 0.f;
-        if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      if (TOP)
-        for (int k = tid; k < a.K; k += G) {
-          a.top_tokens[row * a.K + k] = -1;
-          a.top_logp[row * a.K + k] = -INFINITY;
-        }
-      continue;
-    }
-    float xy = 0.f;
-    if (a.logp && rank == 0 && tid == 0) xy = to_float(x[y]);
+    if (y < 0 || y >= a.V) continue;
     const Slice<T> sl = slice_of(x, a.V, rank, size);
     const int nst = (sl.nv + SV - 1) / SV;
     Run r;
@@ -850,7 +863,7 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
     }
     const int buf = int(round & 1);
     float *keys = keys0 + buf * a.key_floats;
-    if (TOP) bar_wait(&S.empty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
+    if (TOP) bar_wait(&P.hempty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
     for (int k = 0; k < nst; ++k) {
       uint4 v[U];
       bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
@@ -861,7 +874,11 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
       const float mx = add_vectors<T, ENT>(r, v, c);
       if (TOP) keys[k * G + tid] = mx;
     }
-    float floor = r.m;
+    float floor = 0.f;
+    if (TOP) {
+      S.hand[buf].tops[tid] = r.m;
+      floor = of_key(__reduce_min_sync(0xffffffffu, key_of(r.m)));
+    }
     if (tid < 32) {
       add_ends<T>(r, xh, xt, c);
       if (TOP) {
@@ -872,75 +889,86 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
         }
       }
     }
-    const Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, TOP ? &floor : nullptr, size == 1);
-    par ^= 1;
-    if (tid < 32) {
-      const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
-      const float logs = logf(all.s);        // -inf for a row of masks
-      if (tid == 0) {
-        float H = 0.f;
-        if (bad) H = NAN;
-        else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
-        if (rank == 0) {
-          if (a.logp) a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
-          if (a.entropy) a.entropy[row] = H;
-          if (a.saved)
-            reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
-        }
-        if (TOP) {
-          Hand &h = S.hand[buf];
-          h.row = row;
-          h.all = all;
-          h.logs = logs;
-          h.floor = floor;
-        }
-      }
-    }
-    if (TOP) {
-      __syncwarp();
-      if ((tid & 31) == 0) bar_arrive(&S.full[buf]);
-      ++round;
-    }
-  }
-  if (TOP) {  // no more rows
-    const int buf = int(round & 1);
-    bar_wait(&S.empty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
-    if (tid == 0) S.hand[buf].row = -1;
+    const Sums w = join_warp(r, c);
+    if (!TOP) bar_wait(&P.hempty[buf], (round >> 1 & 1) ^ 1, &P.abort, a.errword);
+    if ((tid & 31) == 0) P.warp[buf][tid >> 5] = make_float4(w.m, w.s, w.t, floor);
     __syncwarp();
-    if ((tid & 31) == 0) bar_arrive(&S.full[buf]);
+    if ((tid & 31) == 0) bar_arrive(&P.hfull[buf]);
+    ++round;
   }
 }
 
-// The selecting warps' part: the alternatives of the rows behind the one that is
-// being summed.
-template <typename T, int NW>
-__device__ __forceinline__ void select_rows(const LogpArgs &a, Pipe &P, Select &S, const float *keys0,
-                                            unsigned long long *gather0, int rank, int size, int tid) {
-  constexpr int NS = select_warps<NW>(), NN = NS * 32;
+// The finishing warps' part, a row behind: the join of the sums, the results and
+// the selection of the alternatives.
+template <typename T, int NW, bool TOP, bool ENT>
+__device__ __forceinline__ void finish_rows(const LogpArgs &a, Pipe &P, Select &S, const float *keys0,
+                                            unsigned long long *gather0, int rank, int size, int64_t first, int64_t step,
+                                            int tid) {
+  constexpr int NS = select_warps<NW>(), NN = (TOP ? NS : 1) * 32;
   const unsigned K = unsigned(a.K);
-  for (uint32_t round = 0;; ++round) {
+  const float c = a.scale * LOG2E;
+  uint32_t round = 0;
+  int token = a.tokens && first < a.T ? a.tokens[first] : 0;
+  for (int64_t row = first; row < a.T; row += step) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ld;
+    const int y = token;
+    if (a.tokens && row + step < a.T) token = a.tokens[row + step];
+    if (y < 0 || y >= a.V) {  // the whole cluster takes this way
+      if (rank != 0) continue;
+      if (tid == 0) {
+        if (y >= a.V) atomicOr(a.errword, unsigned(ERR_BOUNDS));
+        if (a.logp) a.logp[row] = 0.f;
+        if (a.entropy) a.entropy[row] = 0.f;
+        if (a.saved) reinterpret_cast<float4 *>(a.saved)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (TOP)
+        for (unsigned k = tid; k < K; k += NN) {
+          a.top_tokens[row * K + k] = -1;
+          a.top_logp[row * K + k] = -INFINITY;
+        }
+      continue;
+    }
     const int buf = int(round & 1);
     const uint32_t phase = round >> 1 & 1;
+    float xy = 0.f;
+    if (a.logp && rank == 0 && tid == 0) xy = to_float(x[y]);
+    const bool ok = bar_wait(&P.hfull[buf], phase, &P.abort, a.errword);
     // all leave together: a warp that stayed would wait for the others
-    if (select_any<NS>(!bar_wait(&S.full[buf], phase, &P.abort, a.errword))) break;
-    const Hand &h = S.hand[buf];
-    const int64_t row = h.row;
-    if (row < 0) break;
-    const bool bad = !(h.all.s < INFINITY);
+    if (TOP ? select_any<NS>(!ok) : !__all_sync(0xffffffffu, ok)) break;
+    const Sums all = join_warps<NW>(P, c, buf, buf, tid < 32, rank, size, a.errword);
+    const bool bad = !(all.s < INFINITY);  // a NaN or +inf among the logits
+    const float logs = logf(all.s);        // -inf for a row of masks
+    if (rank == 0 && tid == 0) {
+      float H = 0.f;
+      if (bad) H = NAN;
+      else if (ENT && all.s > 0.f) H = fmaxf(logs - LN2 * (all.t / all.s), 0.f);
+      if (a.logp) a.logp[row] = bad ? NAN : xy == -INFINITY ? -INFINITY : (xy - all.m) * a.scale - logs;
+      if (a.entropy) a.entropy[row] = H;
+      if (a.saved)
+        reinterpret_cast<float4 *>(a.saved)[row] = make_float4(bad ? NAN : all.m, bad ? NAN : logs, H, 0.f);
+    }
     auto release = [&]() {
       __syncwarp();
-      if ((tid & 31) == 0) bar_arrive(&S.empty[buf]);
+      if ((tid & 31) == 0) bar_arrive(&P.hempty[buf]);
     };
+    ++round;
+    if (!TOP) {
+      release();
+      continue;
+    }
     auto put = [&](unsigned k, unsigned long long b) {
       a.top_tokens[row * K + k] = b ? int32_t(0xffffffffu - uint32_t(b)) : -1;
-      a.top_logp[row * K + k] = bad ? NAN : b ? (of_key(uint32_t(b >> 32)) - h.all.m) * a.scale - h.logs : -INFINITY;
+      a.top_logp[row * K + k] = bad ? NAN : b ? (of_key(uint32_t(b >> 32)) - all.m) * a.scale - logs : -INFINITY;
     };
     if (bad) {
       for (unsigned k = tid; k < K; k += NN) S.best[k] = 0;
       select_sync<NS>();
     } else {
-      const T *x = static_cast<const T *>(a.x) + row * a.ld;
-      select_largest<T, NW>(S, h, keys0 + buf * a.key_floats, x, slice_of(x, a.V, rank, size), K, tid);
+      float floor = P.warp[buf][tid % NW].w;
+#pragma unroll
+      for (int o = NW / 2; o > 0; o >>= 1) floor = fminf(floor, __shfl_xor_sync(0xffffffffu, floor, o));
+      select_largest<T, NW>(S, S.hand[buf], keys0 + buf * a.key_floats, x, slice_of(x, a.V, rank, size), K, floor, all.m,
+                            tid);
     }
     if (size == 1) {
       for (unsigned k = tid; k < K; k += NN) put(k, S.best[k]);
@@ -986,11 +1014,13 @@ __device__ __forceinline__ void select_rows(const LogpArgs &a, Pipe &P, Select &
 }
 
 template <int NW, bool TOP>
-constexpr int logp_threads() { return (NW + 1 + (TOP ? select_warps<NW>() : 0)) * 32; }
+constexpr int finish_warps() { return TOP ? select_warps<NW>() : 1; }
+template <int NW, bool TOP>
+constexpr int logp_threads() { return (NW + 1 + finish_warps<NW, TOP>()) * 32; }
 
-// NW warps compute, one more streams the rows, and where alternatives are wanted
-// a few select them, a row behind: a selection is a chain of short steps, which
-// the next row's sums hide.
+// NW warps compute, one streams the rows, and one (or, where alternatives are
+// wanted, a few) finishes them, a row behind: joining a row's sums and selecting
+// its largest are chains of short steps, which the next row's sums hide.
 template <typename T, int NW, bool TOP, bool ENT>
 __global__ void __launch_bounds__(logp_threads<NW, TOP>(), per_sm<NW>(!TOP)) logp_kernel(const LogpArgs a) {
   constexpr int G = NW * 32;
@@ -1004,19 +1034,15 @@ __global__ void __launch_bounds__(logp_threads<NW, TOP>(), per_sm<NW>(!TOP)) log
   unsigned long long *gather = reinterpret_cast<unsigned long long *>(&S + 1);  // [2][size][K], the first CTA's
   float *keys = reinterpret_cast<float *>(gather + (size > 1 ? 2 * size * a.K : 0));
   if (TOP && tid == 0)
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&S.full[i], NW);
-      bar_init(&S.empty[i], select_warps<NW>());
-      bar_init(&S.gather[i], size);
-    }
-  pipe_init<NW>(P, a.stages, size, cl);
+    for (int i = 0; i < 2; ++i) bar_init(&S.gather[i], size);
+  pipe_init<NW>(P, a.stages, size, NW, finish_warps<NW, TOP>(), cl);
   if (tid < G)
     logp_rows<T, NW, TOP, ENT>(a, P, S, keys, ring, rank, size, first, step);
   else if (tid < G + 32)
     produce<T, NW>(P, ring, a.stages, a.x, a.ld, a.V, a.T, first, step, rank, size, false, a.errword,
                    GivenTokens{a.tokens, a.V, 0});
-  else if (TOP)
-    select_rows<T, NW>(a, P, S, keys, gather, rank, size, tid - G - 32);
+  else
+    finish_rows<T, NW, TOP, ENT>(a, P, S, keys, gather, rank, size, first, step, tid - G - 32);
   if (size > 1) cl.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
@@ -1374,7 +1400,7 @@ __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teac
       e.gather(x0 + (row + step) * a.ld, 0, a.V);
       if (row + 2 * step < a.T) ahead.fetch(a, row + 2 * step);
     }
-    bar_wait(&P.tempty[odd], phase, &P.abort, a.errword);
+    bar_wait(&P.hempty[odd], phase, &P.abort, a.errword);
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
     const int lane = threadIdx.x & 31;
     if (a.tail)  // the marks of the buffer's last row
@@ -1406,7 +1432,7 @@ __device__ __forceinline__ void teacher_rows(const DistillArgs &a, Pipe &P, Teac
       }
     }
     __syncwarp();
-    if (lane == 0) bar_arrive(&P.tfull[odd]);
+    if (lane == 0) bar_arrive(&P.hfull[odd]);
   }
 }
 
@@ -1426,10 +1452,10 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
     const Slice<T> sl = slice_of(x, a.V, rank, size);
     T *out = GRAD ? static_cast<T *>(a.out) + row * a.ldd : nullptr;
     const Teacher &S = teachers[n & 1];
-    bar_wait(&P.tfull[n & 1], uint32_t(n >> 1 & 1), &P.abort, a.errword);
+    bar_wait(&P.hfull[n & 1], uint32_t(n >> 1 & 1), &P.abort, a.errword);
     auto release = [&]() {
       __syncwarp();
-      if ((tid & 31) == 0) bar_arrive(&P.tempty[n & 1]);
+      if ((tid & 31) == 0) bar_arrive(&P.hempty[n & 1]);
     };
     if (S.live == 0) {
       if (rank == 0 && tid == 0) {
@@ -1472,7 +1498,7 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
       }
       add_vectors<T, false>(r, v, c);
     }
-    Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword, nullptr);
+    Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword);
     par ^= 1;
     // tail: `all` is the sum over the tokens outside the teacher's; add the teacher's
     float ltail = 0.f;
@@ -1575,7 +1601,7 @@ __global__ void __launch_bounds__((NW + 3) * 32, per_sm<NW>(false)) distill_kern
   for (int i = tid; i < 2 * mark_bytes / 4; i += (NW + 3) * 32) reinterpret_cast<unsigned *>(marks)[i] = 0u;
   if (tid < 2) teachers[tid].nv = 0;
   for (int i = tid; i < 2 * HASH; i += (NW + 3) * 32) teachers[i / HASH].hash[i % HASH] = -1;
-  pipe_init<NW>(P, a.stages, size, cl);
+  pipe_init<NW>(P, a.stages, size, 1, NW, cl);
   if (tid >= G + 32)
     teacher_rows<T>(a, P, teachers, marks, mark_bytes, rank, size, first, step, (tid - G - 32) / 32);
   else if (tid >= G)
@@ -1671,9 +1697,9 @@ Spread spread(int64_t rows, int cluster, size_t extra, size_t fixed, int per_sm)
   Spread s;
   s.cluster = cluster;
   size_t left = 0;
-  for (;; --per_sm) {  // at least four stages, or two of one CTA alone
+  for (;; --per_sm) {  // at least three stages, or two of one CTA alone
     left = std::min<size_t>(SM / per_sm, 227 * 1024) - fixed;
-    if (left >= extra + 4 * STAGE || per_sm == 1) break;
+    if (left >= extra + 3 * STAGE || per_sm == 1) break;
   }
   s.stages = int(std::min<size_t>((left - extra) / STAGE, MAX_STAGES));
   s.smem = s.stages * STAGE + extra;
