@@ -269,9 +269,9 @@ struct Vec<float> {
 
 constexpr int U = 4;             // vectors of a thread in one stage
 constexpr int MAX_STAGES = 12;
-// CTAs that share an SM: three of eight computing warps where the registers allow it.
+// CTAs that share an SM, by the warps that compute (and what registers allow).
 template <int NW>
-constexpr int per_sm(bool lean) { return NW == 8 ? (lean ? 3 : 2) : 6; }
+constexpr int per_sm(bool lean) { return NW == 8 ? (lean ? 3 : 2) : NW == 4 ? (lean ? 5 : 4) : 6; }
 constexpr int BAR = 1;           // the named barrier of the warps that compute
 constexpr uint64_t TIMEOUT_NS = 4000000000ull;
 
@@ -441,6 +441,24 @@ __device__ __forceinline__ void read_stage(uint4 (&v)[U], const unsigned char *r
   }
 }
 
+// The sums with a thread's vectors added against a far base: rare, and out of
+// line, because the loops over rows should stay in the instruction cache.
+template <typename T, bool ENT>
+__device__ __noinline__ Run add_far_vectors(Run r, uint4 v0, uint4 v1, uint4 v2, uint4 v3, float c) {
+  using X = Vec<T>;
+  static_assert(U == 4, "one argument a vector");
+  const uint4 v[U] = {v0, v1, v2, v3};
+  const float2 mb = both(-r.origin()), c2 = both(c);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float2 x[X::E / 2];
+    X::get(v[u], x);
+#pragma unroll
+    for (int i = 0; i < X::E / 2; ++i) r.template add_far<ENT>(x[i], mb, c2);
+  }
+  return r;
+}
+
 // Adds a thread's vectors to its sums; returns their largest logit.
 template <typename T, bool ENT>
 __device__ __forceinline__ float add_vectors(Run &r, const uint4 (&v)[U], float c) {
@@ -461,14 +479,7 @@ __device__ __forceinline__ float add_vectors(Run &r, const uint4 (&v)[U], float 
       for (int i = 0; i < X::E / 2; ++i) r.template add_near<ENT>(x[i], k2, c2);
     }
   } else {
-    const float2 mb = both(-r.origin());
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 x[X::E / 2];
-      X::get(v[u], x);
-#pragma unroll
-      for (int i = 0; i < X::E / 2; ++i) r.template add_far<ENT>(x[i], mb, c2);
-    }
+    r = add_far_vectors<T, ENT>(r, v[0], v[1], v[2], v[3], c);
   }
   return mx;
 }
@@ -483,7 +494,7 @@ __device__ __forceinline__ Sums join_warps(Pipe &P, float c, int par, int phase,
                                            unsigned *errword) {
   const int lane = threadIdx.x & 31;
   const float4 f = P.warp[par][lane % NW];
-  Sums all = join_lanes<NW == 8 ? 3 : 1>({f.x, f.y, f.z}, c);
+  Sums all = join_lanes<NW == 8 ? 3 : NW == 4 ? 2 : 1>({f.x, f.y, f.z}, c);
   if (size > 1) {
     if (leads && lane < size) {
       const uint32_t to = peer_at(smem_at(&P.part[par][rank]), lane);
@@ -1727,8 +1738,12 @@ poet_status launch_rows(const A &a, const Spread &s, int threads, cudaStream_t s
   return launch_status(what);
 }
 
-// Columns up to which two warps work on a row and not eight.
-constexpr int NARROW = 8192;
+// Columns up to which two warps work on a row.  NARROW, and MEDIUM bytes up to
+// which four do in a distillation: more rows at once hide more of what comes
+// between a row's two passes.  Measured (us, four warps / eight): 8192 rows of
+// 32000 bf16 238 / 252, 1000 of 50257 56 / 63, 2048 of 64000 132 / 119, 2048 of
+// 128000 270 / 260.
+constexpr int NARROW = 8192, MEDIUM = 112 * 1024;
 
 template <typename T, int NW>
 poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
@@ -1763,7 +1778,8 @@ poet_status run_distill(DistillArgs &a, int cluster, cudaStream_t st) {
 template <typename T>
 poet_status run_distill(DistillArgs &a, cudaStream_t st) {
   const int cluster = cluster_of(a.T, a.V);
-  return a.V <= NARROW ? run_distill<T, 2>(a, cluster, st) : run_distill<T, 8>(a, cluster, st);
+  if (a.V <= NARROW) return run_distill<T, 2>(a, cluster, st);
+  return int64_t(a.V) * int64_t(sizeof(T)) <= MEDIUM ? run_distill<T, 4>(a, cluster, st) : run_distill<T, 8>(a, cluster, st);
 }
 
 poet_status check_teacher(const char *what, const int32_t *tokens, const float *values, int32_t K, float value_scale,
