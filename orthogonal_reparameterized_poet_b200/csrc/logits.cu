@@ -423,6 +423,7 @@ __device__ void produce(Pipe &P, const unsigned char *ring, int stages, const vo
 
 template <int NW>
 __device__ __forceinline__ void warps_sync() {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(NW * 32) : "memory");
 }
 
@@ -558,12 +559,14 @@ constexpr int select_warps() { return NW == 8 ? 4 : 2; }
 
 template <int NS>
 __device__ __forceinline__ void select_sync() {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"n"(SELECT_BAR), "n"(NS * 32) : "memory");
 }
 // The same; whether any thread brings true.
 template <int NS>
 __device__ __forceinline__ bool select_any(bool v) {
   unsigned any;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -744,54 +747,96 @@ __device__ void select_largest(Select &S, const Hand &H, const float *keys, cons
     n = S.n;
   }
   if (crowded || n > CAND) {
-    // the exact bound: the largest that K elements reach (elements of groups below it need not be read), then,
-    // among the elements equal to it, the index that leaves K
+    // the exact bound: the largest that K elements reach (elements of groups below it need not be read)
     auto each = [&](float from, auto &&f) {
       for (int k = tid; k < groups; k += NN)
         if (keys[k] >= from)
           for (int u = 0; u < U; ++u) {
             const int v = k / G * SV + u * G + k % G;
-            if (v < sl.nv)
-              for (int i = 0; i < E; ++i) f(to_float(body[int64_t(v) * E + i]), sl.lo + sl.head + v * E + i);
+            if (v < sl.nv) {
+              float2 e[E / 2];
+              Vec<T>::get(*reinterpret_cast<const uint4 *>(body + int64_t(v) * E), e);
+#pragma unroll
+              for (int i = 0; i < E; ++i) f(i & 1 ? e[i / 2].y : e[i / 2].x, sl.lo + sl.head + v * E + i);
+            }
           }
       if (tid < 32) {
         if (tid < sl.head) f(to_float(x[sl.lo + tid]), sl.lo + tid);
         if (sl.tail0 + tid < sl.hi) f(to_float(x[sl.tail0 + tid]), sl.tail0 + tid);
       }
     };
-    auto elements_at = [&](float b) {
-      unsigned c = 0;
-      each(b, [&](float v, int) { c += v >= b; });
-      return select_count<NS>(S, c, tid, flip);
-    };
     uint32_t l = lo, h = key_of(top) + 1;  // at least K reach l, none h
-    while (h - l > 1) {
-      const uint32_t mid = l + (h - l) / 2;
-      if (elements_at(of_key(mid)) >= K) l = mid;
+    for (int step = 0; h - l > 1; ++step) {
+      const float v = 0.5f * of_key(l) + 0.5f * of_key(h - 1);
+      const uint32_t mid = step < 8 ? min(max(key_of(v), l + 1), h - 1) : l + (h - l) / 2;
+      unsigned c = 0;
+      each(of_key(mid), [&](float v, int) { c += v >= of_key(mid); });
+      if (select_count<NS>(S, c, tid, flip) >= K) l = mid;
       else h = mid;
     }
+    // what is above it
     const float b = of_key(l);
-    unsigned c = 0;
-    each(b, [&](float v, int) { c += v > b; });
-    const unsigned left = K - select_count<NS>(S, c, tid, flip);
-    int il = sl.lo, ih = sl.hi;  // fewer than `left` equal ones before il, at least `left` before ih
-    while (ih - il > 1) {
-      const int mid = il + (ih - il) / 2;
-      c = 0;
-      each(b, [&](float v, int i) { c += v == b && i < mid; });
-      if (select_count<NS>(S, c, tid, flip) >= left) ih = mid;
-      else il = mid;
-    }
+    select_sync<NS>();  // all have read S.n
     if (tid == 0) S.n = 0;
     select_sync<NS>();
     each(b, [&](float v, int i) {
-      if (v > b || (v == b && i < ih)) {
-        const unsigned at = atomicAdd(&S.n, 1u);
-        if (at < CAND) S.cand[at] = order_of(v, unsigned(i));
+      if (v > b) {
+        const unsigned to = atomicAdd(&S.n, 1u);
+        if (to < CAND) S.cand[to] = order_of(v, unsigned(i));
       }
     });
     select_sync<NS>();
-    n = min(S.n, unsigned(CAND));
+    // and the first of those equal to it, in their order, as many as are left
+    unsigned taken = S.n;
+    for (int v0 = -1; v0 <= sl.nv && taken < K; v0 = v0 < 0 ? 0 : v0 + NN) {
+      // items of this thread: the elements before the vectors (v0 = -1), a vector, or the elements behind
+      const int v = v0 + tid;
+      float e[E];
+      int at0 = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = -INFINITY;
+      if (v0 < 0) {
+        at0 = sl.lo + tid;
+        if (tid < sl.head) e[0] = to_float(x[at0]);
+      } else if (v < sl.nv) {
+        at0 = sl.lo + sl.head + v * E;
+        float2 f[E / 2];
+        Vec<T>::get(*reinterpret_cast<const uint4 *>(body + int64_t(v) * E), f);
+#pragma unroll
+        for (int i = 0; i < E; ++i) e[i] = i & 1 ? f[i / 2].y : f[i / 2].x;
+      } else if (v == sl.nv) {
+        at0 = sl.tail0;
+        for (int i = 0; i < E; ++i)
+          if (sl.tail0 + i < sl.hi) e[i] = to_float(x[sl.tail0 + i]);
+      }
+      unsigned mine = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) mine += e[i] == b;
+      unsigned upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned u = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((tid & 31) >= o) upto += u;
+      }
+      if ((tid & 31) == 31) S.counts[flip][tid >> 5] = upto;
+      select_sync<NS>();
+      unsigned to = taken + upto - mine, all = 0;
+#pragma unroll
+      for (int w = 0; w < NS; ++w) {
+        if (w < (tid >> 5)) to += S.counts[flip][w];
+        all += S.counts[flip][w];
+      }
+      flip ^= 1;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e[i] == b) {
+          if (to < K) S.cand[to] = order_of(b, unsigned(at0 + i));
+          ++to;
+        }
+      taken += all;
+    }
+    select_sync<NS>();
+    n = min(taken, K);
   } else if (n > 2 * most) {
     // many in the listed groups: a closer bound among the candidates (their order has no ties)
     unsigned long long l = 0, h = ~0ull;
@@ -1763,7 +1808,15 @@ poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
 template <typename T>
 poet_status run_logp(LogpArgs &a, cudaStream_t st) {
   const int cluster = cluster_of(a.T, a.V);
-  return a.V <= NARROW ? run_logp<T, 2>(a, cluster, st) : run_logp<T, 8>(a, cluster, st);
+  // A selection takes as long for short rows as for long ones, so with few alternatives more and smaller CTAs share
+  // an SM; many need the maxima of many threads.  Measured with four warps / eight (us): 8192 rows of 32000 bf16
+  // with 20 142 / 192, with 64 232 / 248; 4096 of 64000 with 20 117 / 127, with 64 173 / 161; 4096 of 128000 with
+  // 64 232 / 223, without 172 / 170; 16384 of 32000 without 194 / 189; with two / eight: 16384 of 8000 with 20
+  // 155 / 313.
+  if (a.V <= NARROW && a.K <= 32) return run_logp<T, 2>(a, cluster, st);
+  if (a.K && (a.K <= 32 || (a.K <= 64 && int64_t(a.V) * int64_t(sizeof(T)) <= MEDIUM)))
+    return run_logp<T, 4>(a, cluster, st);
+  return run_logp<T, 8>(a, cluster, st);
 }
 
 template <typename T, int NW>

@@ -138,6 +138,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *slot, int warps, i
     return;
   }
   if (lane % LANES == 0) slot[warp * N + lane / LANES] = t;
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
   const float4 *s4 = reinterpret_cast<const float4 *>(slot);
   float2 lo = both(0.f), hi = both(0.f);

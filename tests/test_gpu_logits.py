@@ -205,6 +205,21 @@ def test_ties_and_orders(torch, T, V, kind, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,V,K", [(4000, 2000, 20), (4000, 1500, 32), (3000, 3001, 50), (1500, 9000, 128), (700, 40000, 20)])
+def test_alternatives_of_many_rows(torch, T, V, K, dtype):
+    """More rows than the GPU works on at once, rows of every kind of order side by side: ties, few and many distinct
+    values, masks, and ordinary rows."""
+    x, r = _make(torch, T, V, getattr(torch, dtype))
+    kind = torch.arange(T, device="cuda") % 7
+    x[kind == 0] = 0.0
+    x[kind == 1] = (x[kind == 1] > 0).to(x.dtype)
+    x[kind == 2] = torch.linspace(-4, 4, V, device="cuda").to(x.dtype)
+    x[kind == 3] = torch.where(x[kind == 3] < 4.0, -INF, x[kind == 3].float()).to(x.dtype)
+    x[kind == 4] = torch.round(x[kind == 4].float()).to(x.dtype)
+    _check_logprobs(torch, x, r.integers(0, V, T), K)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("T,V", [(3, 50), (5, 2000), (1, 33000)])
 def test_masks(torch, T, V, dtype):
     t = getattr(torch, dtype)
