@@ -41,9 +41,14 @@ struct JointFwdArgs {
   float alpha, beta, eps;
 };
 
-// The sigmoid's exponential and quotient are the fast ones: their few units in
-// the last place are far below an output's rounding.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// The sigmoid's exponential and reciprocal are the hardware's: their few units
+// in the last place are far below a bf16 output's rounding.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 __device__ __forceinline__ float act_of(float g, int sig) { return sig ? sigmoid(g) : g; }
 
 // A thread's own ring of the rows to come.  With S stages every thread copies
@@ -212,22 +217,29 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
     ring.init(1 + (o ? 1 : 0) + (EACH ? 1 : 0));
     if (g.tid * VW >= a.d) ring.zero(S);
   }
+  // the rows' addresses advance a row at a time: those to load, those to write
+  const int c0 = g.tid * VW;
+  const T *lh = h + r0 * a.ldh + c0, *lo = o + r0 * a.ldo + c0, *lg = EACH ? gate + r0 * a.ldg + c0 : nullptr;
+  T *sh = ho + r0 * a.ldho, *sn = n + r0 * a.ldn;
   auto load = [&](int64_t r, int st) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (g.tid + j * a.tpr) * VW;
-      if (c < a.d && r < r1) {
+      const int step = j * a.tpr * VW;
+      if (c0 + step < a.d && r < r1) {
         if constexpr (S > 0) {
-          ring.copy(ring.at(st, 0, j), h + r * a.ldh + c);
-          if (o) ring.copy(ring.at(st, 1, j), o + r * a.ldo + c);
-          if (EACH) ring.copy(ring.at(st, 2, j), gate + r * a.ldg + c);
+          ring.copy(ring.at(st, 0, j), lh + step);
+          if (o) ring.copy(ring.at(st, 1, j), lo + step);
+          if (EACH) ring.copy(ring.at(st, 2, j), lg + step);
         } else {
-          vh.v[j].load(h + r * a.ldh + c);
-          if (o) vo.v[j].load(o + r * a.ldo + c);
-          if (EACH) vg.v[j].load(gate + r * a.ldg + c);
+          vh.v[j].load(lh + step);
+          if (o) vo.v[j].load(lo + step);
+          if (EACH) vg.v[j].load(lg + step);
         }
       }
     }
+    lh += a.ldh;
+    lo += a.ldo;
+    if (EACH) lg += a.ldg;
     if constexpr (S > 0) ring.commit();
   };
   int st = 0;
@@ -308,7 +320,8 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
       }
 #pragma unroll
       for (int p = 0; p < NP; ++p) x[p] = fma2(mul2(q[p], both(ro)), wq[p], mul2(x[p], alpha));
-      L::put(ho + r * a.ldho, g.tid, a.tpr, a.d, x);
+      L::put(sh, g.tid, a.tpr, a.d, x);
+      sh += a.ldho;
     }
     if constexpr (S > 0) {
       load(r + S - 1, st == 0 ? S - 1 : st - 1);
@@ -328,7 +341,8 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
       const float2 rn = both(inv_sqrt(fmaf(s[0], inv_d, a.eps)));
 #pragma unroll
       for (int p = 0; p < NP; ++p) x[p] = mul2(mul2(x[p], rn), wn[p]);
-      L::put(n + r * a.ldn, g.tid, a.tpr, a.d, x);
+      L::put(sn, g.tid, a.tpr, a.d, x);
+      sn += a.ldn;
     }
   }
 }
