@@ -196,8 +196,8 @@ __device__ __forceinline__ void zero_slots(float *p, int n) {
 
 template <typename T, int VW, int NV, int S, int GK, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArgs a) {
-  __shared__ __align__(16) float red[8][2][32];
-  zero_slots(red[0][0], 8 * 2 * 32);
+  __shared__ __align__(16) float red[8][2][2 * 32];
+  zero_slots(red[0][0], 8 * 2 * 2 * 32);
   const Group g(a.tpr);
   using L = Lane<T, VW, NV>;
   constexpr int NP = L::NP;
@@ -262,6 +262,37 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
   float gval = 1.f;
   const float inv_d = 1.f / float(a.d);
   const float2 alpha = both(a.alpha);
+  const bool post = o && a.post;
+  auto read = [&](L &v, int stage, int place) {
+    if constexpr (S > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) ring.read(v.v[j], ring.at(stage, place, j));
+    }
+  };
+  // One exchange a row: the sum over row r's new stream together with the one
+  // over row r + 1's branch (both wait for all the row's threads).
+  float2 s2 = both(0.f);
+  float s[2] = {0.f, 0.f};
+  auto branch_sum = [&](int stage) {
+    float2 q[NP];
+    read(vo, stage, 1);
+    vo.get(q);
+    s2 = both(0.f);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) s2 = fma2(q[p], q[p], s2);
+    s[0] = s2.x + s2.y;
+  };
+  auto exchange = [&]() {
+    row_sum<2>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+    float *const was = slot;
+    slot = other;
+    other = was;
+  };
+  if constexpr (S > 0) ring.wait();
+  if (post) {
+    branch_sum(0);
+    exchange();
+  }
   for (int64_t r = r0; r < r1; ++r) {
     if (r == gnext) {  // the next gate row
       if (r != r0) ++grow;
@@ -282,34 +313,17 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
           wq[p] = mul2(wq[p], make_float2(act_of(gv[p].x, a.gate_sigmoid), act_of(gv[p].y, a.gate_sigmoid)));
       }
     }
-    if constexpr (S > 0) {
-      ring.wait();
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        ring.read(vh.v[j], ring.at(st, 0, j));
-        if (o) ring.read(vo.v[j], ring.at(st, 1, j));
-        if (EACH) ring.read(vg.v[j], ring.at(st, 2, j));
-      }
-    }
     float2 x[NP];
+    read(vh, st, 0);
     vh.get(x);
     if (o) {
       float2 q[NP];
+      read(vo, st, 1);
       vo.get(q);
-      float ro = gval;
-      if (a.post) {
-        float2 s2 = both(0.f);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) s2 = fma2(q[p], q[p], s2);
-        float s[1] = {s2.x + s2.y};
-        row_sum<1>(s, slot, g.warps, g.warp, g.bar, a.tpr);
-        float *const was = slot;
-        slot = other;
-        other = was;
-        ro *= inv_sqrt(fmaf(s[0], inv_d, a.eps));
-      }
+      const float ro = post ? gval * inv_sqrt(fmaf(s[0], inv_d, a.eps)) : gval;
       if (EACH) {
         float2 gv[NP];
+        read(vg, st, 2);
         vg.get(gv);
         if (a.gate_sigmoid) {
 #pragma unroll
@@ -326,19 +340,20 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
     if constexpr (S > 0) {
       load(r + S - 1, st == 0 ? S - 1 : st - 1);
       st = st + 1 == S ? 0 : st + 1;
+      ring.wait();  // row r + 1 is there
     } else {
       load(r + 1, 0);
     }
-    if (n) {
-      float2 s2 = both(0.f);
+    if (!n && !post) continue;
+    s2 = both(0.f);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) s2 = fma2(x[p], x[p], s2);
-      float s[1] = {s2.x + s2.y};
-      row_sum<1>(s, slot, g.warps, g.warp, g.bar, a.tpr);
-      float *const was = slot;
-      slot = other;
-      other = was;
-      const float2 rn = both(inv_sqrt(fmaf(s[0], inv_d, a.eps)));
+    for (int p = 0; p < NP; ++p) s2 = fma2(x[p], x[p], s2);
+    s[1] = s2.x + s2.y;
+    s[0] = 0.f;
+    if (post) branch_sum(st);  // behind the last row: of what is there, not used
+    exchange();
+    if (n) {
+      const float2 rn = both(inv_sqrt(fmaf(s[1], inv_d, a.eps)));
 #pragma unroll
       for (int p = 0; p < NP; ++p) x[p] = mul2(mul2(x[p], rn), wn[p]);
       L::put(sn, g.tid, a.tpr, a.d, x);
@@ -365,8 +380,8 @@ struct JointBwdArgs {
 
 template <typename T, int VW, int NV, int S, int GK, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArgs a) {
-  __shared__ __align__(16) float red[8][2][4 * 32];
-  zero_slots(red[0][0], 8 * 2 * 4 * 32);
+  __shared__ __align__(16) float red[8][2][5 * 32];
+  zero_slots(red[0][0], 8 * 2 * 5 * 32);
   const Group g(a.tpr);
   using L = Lane<T, VW, NV>;
   constexpr int NP = L::NP;
@@ -463,43 +478,17 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
 #pragma unroll
     for (int p = 0; p < NP; ++p) ag[p] = both(0.f);
   };
-  float ga_row = 1.f, sl_row = 1.f;  // a row gate's value and slope
-  int64_t gnext = a.gate_kind != POET_GATE_NONE && !EACH ? r0 : a.T;
-  for (int64_t r = r0; r < r1; ++r) {
-    if (r == gnext) {  // the next gate row
-      if (r != r0) {
-        flush_gate();
-        ++grow;
-      }
-      gnext = (grow + 1) * a.gate_rows;
-      if (!SHARED) {
-        ga_row = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
-        sl_row = a.gate_sigmoid ? ga_row * (1.f - ga_row) : 1.f;
-      } else {
+  auto fetch = [&](L &v, int place) {
+    if constexpr (S > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int c = (g.tid + j * a.tpr) * VW;
-          if (c < a.d) vg.v[j].load(gate + grow * a.ldg + c);
-        }
-      }
+      for (int j = 0; j < NV; ++j) ring.read(v.v[j], ring.at(st, place, j));
     }
-    // First pass over the row: its sums.  The second pass takes the operands from
-    // the ring again rather than hold them in registers across the exchange.
-    auto fetch = [&](L &v, int place) {
-      if constexpr (S > 0) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) ring.read(v.v[j], ring.at(st, place, j));
-      }
-    };
-    if constexpr (S > 0) ring.wait();
-    if (EACH && S > 0 && !GR) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (g.tid + j * a.tpr) * VW;
-        if (c < a.d) vg.v[j].load(gate + r * a.ldg + c);
-      }
-    }
-    float s[4] = {0.f, 0.f, 0.f, 0.f};  // sum h'^2, sum u h', sum o^2
+  };
+  // The first sums of the row in stage st: h'^2, u h', o^2.  Each row's operands
+  // are read from the ring twice, for its sums and for what follows from them,
+  // rather than held in registers across the exchange.
+  float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+  auto first_sums = [&]() {
     if (dn) {
       float2 x[NP], y[NP], wn[NP], s0 = both(0.f), s1 = both(0.f);
       fetch(vh, 0);
@@ -523,9 +512,48 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
       for (int p = 0; p < NP; ++p) s2 = fma2(x[p], x[p], s2);
       s[2] = s2.x + s2.y;
     }
-    row_sum<4>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+  };
+  // One exchange a row: the sums that row r's branch gradient needs (v ph, and
+  // that of a row gate's gradient before its slope) with the first ones of row r + 1.
+  const bool fifth = GK == GK_ROW && dgate;
+  auto exchange = [&]() {
+    row_sum_5(s, fifth, slot, g.warps, g.warp, g.bar, a.tpr);
+    float *const was = slot;
+    slot = other;
+    other = was;
+  };
+  if constexpr (S > 0) ring.wait();
+  if (r0 < r1) first_sums();
+  exchange();
+  float ga_row = 1.f, sl_row = 1.f;  // a row gate's value and slope
+  int64_t gnext = a.gate_kind != POET_GATE_NONE && !EACH ? r0 : a.T;
+  for (int64_t r = r0; r < r1; ++r) {
+    if (r == gnext) {  // the next gate row
+      if (r != r0) {
+        flush_gate();
+        ++grow;
+      }
+      gnext = (grow + 1) * a.gate_rows;
+      if (!SHARED) {
+        ga_row = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
+        sl_row = a.gate_sigmoid ? ga_row * (1.f - ga_row) : 1.f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = (g.tid + j * a.tpr) * VW;
+          if (c < a.d) vg.v[j].load(gate + grow * a.ldg + c);
+        }
+      }
+    }
     const float rn = inv_sqrt(fmaf(s[0], inv_d, a.eps)), mn = s[1] * rn * inv_d;  // 1 / r', mean(u nh)
     const float ro = a.post ? inv_sqrt(fmaf(s[2], inv_d, a.eps)) : 1.f;           // 1 / r
+    if (EACH && S > 0 && !GR) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (g.tid + j * a.tpr) * VW;
+        if (c < a.d) vg.v[j].load(gate + r * a.ldg + c);
+      }
+    }
     float2 t[NP], q[NP];  // t, then v; ph
     if (dhp) {
       fetch(vd, sd);
@@ -555,7 +583,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
       for (int p = 0; p < NP; ++p) out[p] = mul2(t[p], alpha);
       L::put(dh + r * a.lddh, g.tid, a.tpr, a.d, out);
     }
-    float w[2] = {0.f, 0.f};  // sum v ph, sum of the row gate's gradient before its slope
+    s[3] = s[4] = 0.f;
     if (o) {
       float2 w0 = both(0.f), w1 = both(0.f), dg[NP], wq[NP];
       fetch(vo, so);
@@ -585,37 +613,30 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
         }
       }
       if (EACH && dgate) L::put(dgate + r * a.lddg, g.tid, a.tpr, a.d, dg);
-      w[0] = w0.x + w0.y;
-      w[1] = w1.x + w1.y;
+      s[3] = w0.x + w0.y;
+      s[4] = w1.x + w1.y;
     }
     if constexpr (S > 0) {
       load(r + S - 1, st == 0 ? S - 1 : st - 1);
       st = st + 1 == S ? 0 : st + 1;
+      ring.wait();  // row r + 1 is there
     } else {
       load(r + 1, 0);
     }
-    if (!o) {  // one sum a row: its buffers alternate
-      float *const was = slot;
-      slot = other;
-      other = was;
-      continue;
-    }
-    if (a.post || (dgate && a.gate_kind == POET_GATE_ROW)) {
-      row_sum<2>(w, other, g.warps, g.warp, g.bar, a.tpr);
-    } else if (g.warps > 1) {  // the first sum's buffer is written again in the next row
-      asm volatile("bar.sync %0, %1;" ::"r"(g.bar), "r"(a.tpr) : "memory");
-    }
+    first_sums();  // behind the last row: of what is there, not used
+    exchange();
+    if (!o) continue;
     if (a.post) {
-      const float2 mo = both(-w[0] * inv_d);  // -mean(v ph)
+      const float2 mo = both(-s[3] * inv_d);  // -mean(v ph)
 #pragma unroll
       for (int p = 0; p < NP; ++p) t[p] = mul2(fma2(q[p], mo, t[p]), both(ro));
     }
     L::put(d_o + r * a.lddo, g.tid, a.tpr, a.d, t);
     if (!EACH && !SHARED && dgate) {
       if (a.gate_rows == 1) {
-        if (g.tid == 0) dgate[r * a.lddg] = from_float<T>(w[1] * sl_row);
+        if (g.tid == 0) dgate[r * a.lddg] = from_float<T>(s[4] * sl_row);
       } else {
-        ag_row += w[1] * sl_row;
+        ag_row += s[4] * sl_row;
       }
     }
   }

@@ -158,4 +158,43 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *slot, int warps, i
   }
 }
 
+// The same for four values and, where `fifth` is true, one more.  slot: 5 * 32
+// floats, the fifth values behind the others.
+__device__ __forceinline__ void row_sum_5(float (&v)[5], bool fifth, float *slot, int warps, int warp, int bar,
+                                          int threads) {
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16, up = lane & 8;
+  const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+  const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+  float t = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (fifth) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[4] += __shfl_xor_sync(0xffffffffu, v[4], o);
+  }
+  if (warps == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * 8);
+    return;
+  }
+  if (lane % 8 == 0) slot[warp * 4 + lane / 8] = t;
+  if (fifth && lane == 0) slot[128 + warp] = v[4];
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  const float4 *s4 = reinterpret_cast<const float4 *>(slot);
+  float2 lo = both(0.f), up2 = both(0.f);
+#pragma unroll 2
+  for (int i = 0; i < warps; ++i) {
+    const float4 f = s4[i];
+    lo = add2(lo, make_float2(f.x, f.y));
+    up2 = add2(up2, make_float2(f.z, f.w));
+  }
+  v[0] = lo.x; v[1] = lo.y; v[2] = up2.x; v[3] = up2.y;
+  if (fifth) {
+    v[4] = 0.f;
+    for (int i = 0; i < warps; ++i) v[4] += slot[128 + i];
+  }
+}
+
 }  // namespace poet
