@@ -4,7 +4,8 @@
 
 Each .cu under csrc/ is compiled to an object under _build/ (in parallel),
 then linked into orthogonal_reparameterized_poet_b200/libpoet.so.  Objects
-are rebuilt when their source, a header, or this file is newer.
+are rebuilt when their source, a header, or this file is newer.  csrc/binding.cpp
+becomes _binding.so beside it (the host compiler, torch's headers).
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpoet.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -48,6 +50,28 @@ def _compile(src, force):
     return obj
 
 
+def _binding(force):
+    """The binding of the operators on torch tensors, linked against libpoet.so beside it."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not (force or _stale(BINDING, [src] + _headers())):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    include = cpp_extension.include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in include], src,
+           "-o", BINDING, f"-L{PKG}", "-l:libpoet.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding failed to compile:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -58,6 +82,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _binding(force)
     if verbose:
         print(LIB)
     return LIB

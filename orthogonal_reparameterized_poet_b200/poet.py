@@ -8,6 +8,7 @@ host fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -21,6 +22,9 @@ OK, EINVAL, ECUDA, ETIMEOUT, ENOMEM_WS, EBOUNDS = 0, 1, 2, 3, 4, 5
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpoet.so")
 _lib = None
+# the common call of the operators around the blocks (csrc/binding.cpp)
+_BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+_binding = None
 
 
 class PoetError(RuntimeError):
@@ -181,6 +185,21 @@ def lib() -> ctypes.CDLL:
             f.argtypes = args
         _lib = L
     return _lib
+
+
+def _native():
+    """The compiled binding of the operators around the blocks (raises if it is not built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        if not os.path.exists(_BINDING_PATH):
+            raise RuntimeError(f"_binding.so not built at {_BINDING_PATH}; run "
+                               "`python -m orthogonal_reparameterized_poet_b200.build`")
+        spec = importlib.util.spec_from_file_location("_binding", _BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 def _check(status):
@@ -776,6 +795,10 @@ def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, p
     takes o as it is; pre_norm=False leaves n out (None).  o=None: n = rmsnorm(h) w_pre alone (h' is None).
     h_out and n are allocated where they are not given.  stream: the stream to run on (None: the current one);
     what is allocated belongs to it."""
+    if o is not None and h_out is None and n is None and stream is None and (pre_norm or w_pre is None):
+        r = _native().joint_forward(o, h, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps, pre_norm)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     J, dev, shape, t, po, ldo, ph, ldh, pg, ldg, like = _joint(h, o, gate, w_post, w_pre, post_norm, gate_act,
                                                                gate_rows, alpha, beta, eps)
     if o is None and (h_out is not None or not pre_norm):
@@ -812,6 +835,11 @@ def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_
     be None).  o, gate and the options are the forward's, h_out its result (h where o is None).  Gradients of
     what the joint does not have are None; the others are allocated where they are not given (ws too).  Two
     calls that may run at the same time need a ws each."""
+    if o is not None and dh is d_o is dgate is dw_post is dw_pre is ws is stream is None:
+        r = _native().joint_backward(o, h_out, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps,
+                                     dh_out, dn)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     J, dev, shape, t, po, ldo, ph, ldh, pg, ldg, like = _joint(h_out, o, gate, w_post, w_pre, post_norm, gate_act,
                                                                gate_rows, alpha, beta, eps)
     if dn is None and w_pre is not None:
@@ -908,6 +936,10 @@ def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, save
     tokens: int32 [T] or None (then logp is None); a negative token leaves its row out.  topk: how many
     alternatives to list (0: none).  entropy=False leaves the entropy out (None).  saved: float32 [T, 4],
     what token_logprobs_grad reads (allocated where it is not given)."""
+    if saved is None and stream is None:
+        r = _native().token_logprobs(logits, tokens, topk, scale, entropy)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     dev, dt, T, V, px, ld = _logits(logits)
     pt = _per_row(tokens, "tokens", T, _I32, dev)
     st = _stream_on(stream, dev)
@@ -930,6 +962,10 @@ def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, save
 def token_logprobs_grad(logits, tokens, saved, dlogp=None, dentropy=None, *, scale=1.0, dlogits=None, stream=None):
     """dlogits for the gradients dlogp and dentropy (float32 [T], either may be None) of token_logprobs's
     results; saved: the forward's.  dlogits may be logits."""
+    if dlogits is None and stream is None:
+        r = _native().token_logprobs_grad(logits, tokens, saved, dlogp, dentropy, scale)
+        if r is not None:
+            return r if type(r) is not int else _check(r)
     dev, dt, T, V, px, ld = _logits(logits)
     pt = _per_row(tokens, "tokens", T, _I32, dev)
     ps = _operand(saved, "saved", (T, 4), _F32, dev, False)[0]
@@ -957,6 +993,10 @@ def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tai
     (tail=False: renormalized over the entries) or log probabilities (tail=True: what they leave of the mass
     is one more outcome).  grad=True (or dlogits given): dlogits is the gradient of sum dloss * loss (dloss:
     float32 [T], None = 1), formed in the same pass; otherwise None.  dlogits may be logits."""
+    if dlogits is None and saved is None and stream is None:
+        r = _native().distill_topk(logits, teacher_tokens, teacher_values, value_scale, tail, scale, dloss, grad)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
     pw = _per_row(dloss, "dloss", T, _F32, dev)
@@ -974,6 +1014,10 @@ def distill_topk(logits, teacher_tokens, teacher_values, *, value_scale=1.0, tai
 def distill_topk_grad(logits, teacher_tokens, teacher_values, saved, dloss=None, *, value_scale=1.0, tail=False,
                       scale=1.0, dlogits=None, stream=None):
     """dlogits = the gradient of sum dloss * loss, from the forward's saved.  dlogits may be logits."""
+    if dlogits is None and stream is None:
+        r = _native().distill_topk_grad(logits, teacher_tokens, teacher_values, value_scale, tail, scale, saved, dloss)
+        if r is not None:
+            return r if type(r) is not int else _check(r)
     dev, dt, T, V, px, ld = _logits(logits)
     pt, pv, K = _teacher(teacher_tokens, teacher_values, T, dev)
     pw = _per_row(dloss, "dloss", T, _F32, dev)
