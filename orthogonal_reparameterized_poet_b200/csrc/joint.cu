@@ -673,8 +673,20 @@ __global__ void __launch_bounds__(32 * SUM_LANES) joint_sum_kernel(const JointSu
   const int col = blockIdx.x * 32 + threadIdx.x;
   if (!src || int(blockIdx.x) * 32 >= width) return;
   float s = 0.f;
-  if (col < width)
-    for (int64_t i = threadIdx.y; i < count; i += SUM_LANES) s += src[i * width + col];
+  if (col < width) {
+    constexpr int AHEAD = 8;  // loads in flight
+    const int64_t stride = int64_t(SUM_LANES) * width;
+    const float *p = src + int64_t(threadIdx.y) * width + col;
+    int left = int((count - threadIdx.y + SUM_LANES - 1) / SUM_LANES);
+    for (; left >= AHEAD; left -= AHEAD, p += AHEAD * stride) {
+      float v[AHEAD];
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) v[q] = p[q * stride];
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) s += v[q];
+    }
+    for (; left > 0; --left, p += stride) s += *p;
+  }
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || col >= width) return;
@@ -731,8 +743,9 @@ BwdPlan bwd_plan(const poet_joint *J, int64_t T, int64_t most) {
   return p;
 }
 
-// CTAs that an SM holds (what the kernels' launch bounds ask for).
-int fwd_resident(int threads) { return threads <= 256 ? 3 : 1; }
+// CTAs that an SM holds (what the kernels' launch bounds ask for: 80 registers a
+// thread in the forward up to 256 threads).
+int fwd_resident(int threads) { return threads <= 256 ? 65536 / (80 * threads) : 1; }
 int bwd_resident(int threads) { return threads <= 320 ? 2 : 1; }
 
 // Most groups of rows in the backward: what runs at once, and at least four rows

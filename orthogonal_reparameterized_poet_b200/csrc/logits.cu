@@ -1704,10 +1704,19 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
 
 // CTAs of a row.  One per row where there are rows enough for every SM; with
 // fewer, a row is split so that the GPU has two CTAs per SM or the slices fall
-// to 4096 columns, whichever comes first.  A slice has at most SLICE columns.
-int cluster_of(int64_t T, int V) {
+// to 4096 columns, whichever comes first.  Alternatives are selected from every
+// slice and merged, which costs more the more of both there are: their slices
+// stay above 16384 columns, and at most four and 256 / K share a row.  Measured
+// (us, 1 / 2 / 4 / 8 CTAs a row): 4 rows of 32000 without 4.8 / 4.7 / 4.2 / 4.3,
+// with 20 10.7 / 10.8 / 11.5 / 16.5; 4 of 128000 without 10.4 / 7.5 / 5.7 / 4.8,
+// with 20 22.5 / 16.6 / 14.5 / 17.9, with 128 23.5 / 21.2 / 22.6 / 40.9.  A slice
+// has at most SLICE columns.
+int cluster_of(int64_t T, int V, int K = 0) {
+  const int least = K ? 16384 : 4096, most = K ? std::max(1, std::min(4, 256 / K)) : MAX_CLUSTER;
   int c = 1;
-  while (c < MAX_CLUSTER && ((T * c < int64_t(num_sms()) * 2 && V / (2 * c) >= 4096) || V > int64_t(SLICE) * c)) c *= 2;
+  while (c < MAX_CLUSTER &&
+         ((2 * c <= most && T * c < int64_t(num_sms()) * 2 && V / (2 * c) >= least) || V > int64_t(SLICE) * c))
+    c *= 2;
   return c;
 }
 
@@ -1807,7 +1816,7 @@ poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
 }
 template <typename T>
 poet_status run_logp(LogpArgs &a, cudaStream_t st) {
-  const int cluster = cluster_of(a.T, a.V);
+  const int cluster = cluster_of(a.T, a.V, a.K);
   // A selection takes as long for short rows as for long ones, so with few alternatives more and smaller CTAs share
   // an SM; many need the maxima of many threads.  Measured with four warps / eight (us): 8192 rows of 32000 bf16
   // with 20 142 / 192, with 64 232 / 248; 4096 of 64000 with 20 117 / 127, with 64 173 / 161; 4096 of 128000 with
