@@ -427,6 +427,16 @@ __device__ __forceinline__ void warps_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(NW * 32) : "memory");
 }
 
+// Gives a stage back to the producer, by a warp that has used what it read from
+// it.  The stage's next bytes come through the async proxy, so the reads, which
+// are generic, are fenced against it; an arrival alone was seen to pass loads
+// whose values were not used yet, and those then found the next bytes.
+__device__ __forceinline__ void give_back(uint64_t *empty) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(empty);
+}
+
 // A stage's vectors of this thread; those behind the slice's end are masked.
 template <typename T, int NW>
 __device__ __forceinline__ void read_stage(uint4 (&v)[U], const unsigned char *ring, int st, int left) {
@@ -924,10 +934,9 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
       uint4 v[U];
       bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
       read_stage<T, NW>(v, ring, at.st, sl.nv - k * SV);
-      __syncwarp();
-      if ((tid & 31) == 0) bar_arrive(&P.empty[at.st]);
-      at.next(a.stages);
       const float mx = add_vectors<T, ENT>(r, v, c);
+      give_back(&P.empty[at.st]);
+      at.next(a.stages);
       if (TOP) keys[k * G + tid] = mx;
     }
     float floor = 0.f;
@@ -1539,11 +1548,6 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
       uint4 v[U];
       bar_wait(&P.full[at.st], at.ph, &P.abort, a.errword);
       read_stage<T, NW>(v, ring, at.st, sl.nv - k * SV);
-      if (!stays) {
-        __syncwarp();
-        if ((tid & 31) == 0) bar_arrive(&P.empty[at.st]);
-      }
-      at.next(a.stages);
       if (a.tail) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -1553,6 +1557,8 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
         }
       }
       add_vectors<T, false>(r, v, c);
+      if (!stays) give_back(&P.empty[at.st]);
+      at.next(a.stages);
     }
     Sums all = join_row<NW>(P, r, c, par, rank, size, a.errword);
     par ^= 1;
@@ -1610,9 +1616,6 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
         uint4 v[U];
         if (!stays) bar_wait(&P.full[from.st], from.ph, &P.abort, a.errword);
         read_stage<T, NW>(v, ring, from.st, sl.nv - k * SV);
-        __syncwarp();
-        if ((tid & 31) == 0) bar_arrive(&P.empty[from.st]);
-        from.next(a.stages);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int i = k * SV + u * G + tid;
@@ -1628,6 +1631,8 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
             for (int e = 0; e < E; ++e) to[int64_t(i) * E + e] = from_float<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
           }
         }
+        give_back(&P.empty[from.st]);
+        from.next(a.stages);
       }
       warps_sync<NW>();
       if (!empty) write_teacher(S, a, out, sl.lo, sl.hi, bad ? NAN : M, logs, g, G);

@@ -414,6 +414,39 @@ def test_distill_shapes(torch, T, V, K, tail, dtype):
     _check_distill(torch, x, tokens, values, r, tail)
 
 
+@pytest.mark.parametrize("V,K", [(3000, 20), (32000, 64), (50257, 20), (70000, 33)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_of_many_rows(torch, V, K, tail):
+    """More rows than the GPU works on at once, of every kind of width, twice: some rows left out.  Distinct rows repeat,
+    so that the oracle need not see each."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    few, T = 24, 1800
+    base, r = _make(torch, few, V, torch.bfloat16)
+    tokens, values = _teacher_case(r, few, V, K, tail)
+    tokens[5] = -1
+    order = torch.from_numpy(r.integers(0, few, T)).cuda()
+    x, tt, tv = base[order].contiguous(), torch.from_numpy(tokens).cuda()[order], torch.from_numpy(values).cuda()[order]
+    want, dwant = _check_distill(torch, base, tokens, values, r, tail, weights=False)
+    plain, none, _ = poet.distill_topk(base, torch.from_numpy(tokens).cuda(), torch.from_numpy(values).cuda(), tail=tail)
+    for _ in range(4):
+        loss, d, saved = poet.distill_topk(x, tt, tv, tail=tail, grad=True)
+        alone = poet.distill_topk(x, tt, tv, tail=tail)[0]
+        tk = torch.where(tt[:, 0] < 0, 0, tt[:, 0]).contiguous()
+        logp, H, top, topl, sv = poet.token_logprobs(x, tk, topk=5)
+        poet.poet_sync_status()
+        # the sums may be split otherwise with more rows: compared within the derived bound of the sums
+        bound = 4 * _steps(V) * U * (1 + want.abs()[order].double())
+        assert ((loss - want[order]).double().abs() <= bound).all() and ((alone - want[order]).double().abs() <= bound).all()
+        half = torch.finfo(x.dtype).eps / 2
+        scale = dwant[order].double().abs()
+        assert ((d.double() - dwant[order].double()).abs() <= 2 * half * scale + 8 * _steps(V) * U * scale + 1e-9).all()
+        mean = torch.log_softmax(x.double(), 1)
+        at = mean.gather(1, tk.long()[:, None])[:, 0]
+        assert ((logp.double() - at).abs() <= (_steps(V) + 64) * U * (1 + at.abs())).all()
+        assert torch.equal(top.long(), x.sort(dim=1, descending=True, stable=True)[1][:, :5])
+
+
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("ragged,twice", [(True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("scale,value_scale", [(1.0, 1.0), (0.5, 1.3)])
