@@ -502,7 +502,10 @@ POET_API poet_status poet_joint_backward(const poet_joint *J, const void *o, int
  *    the tokens outside the teacher's}.  The third is poet_token_logprobs's,
  *    the fourth poet_distill_topk's (tail); a call writes 0 in what is not its
  *    own.  It is what the backward reads.
- *  - Sums are float and run in a fixed order. */
+ *  - Sums are float and run in a fixed order: the same call gives the same bits.
+ *    How a row is split, and so the last bits, depends on T, V and topk.
+ *  - Waits inside the kernels are bounded; one that ran out is reported by
+ *    poet_sync_status (POET_ETIMEOUT) and the call's results are void. */
 
 /* logp[t] = ln p of tokens[t]; entropy[t] = -sum p ln p; top_tokens, top_logp
  * (T x topk, 0 <= topk <= 128): the topk most likely tokens of the row in
