@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
     s[0] = s2.x + s2.y;
   };
   auto exchange = [&]() {
-    row_sum<2>(s, slot, g.warps, g.warp, g.bar, a.tpr);
+    row_sum_2(s, slot, g.warps, g.warp, g.bar, a.tpr);
     float *const was = slot;
     slot = other;
     other = was;

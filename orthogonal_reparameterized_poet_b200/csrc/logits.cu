@@ -192,7 +192,7 @@ __device__ __forceinline__ Sums join_warp(Run &r, float c) {
   const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(r.m)));
   if (m > -INFINITY) r.shift(r.at(m, c));
   float v[2] = {r.s.x + r.s.y, r.t.x + r.t.y};
-  row_sum<2>(v, nullptr, 1, 0, 0, 32);
+  row_sum_2(v, nullptr, 1, 0, 0, 32);
   return {m, v[0], v[1]};
 }
 

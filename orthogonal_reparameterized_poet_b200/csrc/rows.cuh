@@ -105,57 +105,38 @@ __device__ __forceinline__ float inv_sqrt(float x) {
   return y > 0.f ? fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y) : y;
 }
 
-// Sums v[0..N), N = 1, 2 or 4, over the `warps` warps that share a row; every
-// thread gets the totals, added in one fixed order.  Within a warp several
-// values are summed by one butterfly: its first steps exchange halves of the
-// values, so that N values take 4 + N (N = 1: 5) shuffles.  One barrier:
-// `slot` (N * 32 floats, 16-byte aligned, zero behind the last warp) alternates
-// between two buffers, and a buffer is written again only after the barrier of
-// the other one, which no thread passes before all have read the first.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float *slot, int warps, int warp, int bar, int threads) {
+// Sums two values over the `warps` warps that share a row; every thread gets the
+// totals, added in one fixed order.  Within a warp one butterfly sums both: its
+// first step exchanges one value for the other, which takes six shuffles for
+// both.  One barrier: `slot` (2 * 32 floats, 16-byte aligned, zero behind the
+// last warp) alternates between two buffers, and a buffer is written again only
+// after the barrier of the other one, which no thread passes before all have
+// read the first.
+__device__ __forceinline__ void row_sum_2(float (&v)[2], float *slot, int warps, int warp, int bar, int threads) {
   const int lane = threadIdx.x & 31;
-  float t;
-  if constexpr (N == 4) {
-    const bool hi = lane & 16, up = lane & 8;
-    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
-    const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
-    t = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
-  } else if constexpr (N == 2) {
-    const bool hi = lane & 16;
-    t = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
-    t += __shfl_xor_sync(0xffffffffu, t, 8);
-  } else {
-    t = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
-    t += __shfl_xor_sync(0xffffffffu, t, 8);
-  }
+  const bool hi = lane & 16;
+  float t = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  constexpr int LANES = 32 / N;  // lanes that hold one value's total
+  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if (warps == 1) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = N == 1 ? t : __shfl_sync(0xffffffffu, t, i * LANES);
+    v[0] = __shfl_sync(0xffffffffu, t, 0);
+    v[1] = __shfl_sync(0xffffffffu, t, 16);
     return;
   }
-  if (lane % LANES == 0) slot[warp * N + lane / LANES] = t;
+  if (lane % 16 == 0) slot[warp * 2 + lane / 16] = t;
   __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
   const float4 *s4 = reinterpret_cast<const float4 *>(slot);
-  float2 lo = both(0.f), hi = both(0.f);
-  const int quads = (warps * N + 3) / 4;
+  float2 a = both(0.f), b = both(0.f);
+  const int quads = (warps + 1) / 2;
 #pragma unroll 2
   for (int i = 0; i < quads; ++i) {
     const float4 f = s4[i];
-    lo = add2(lo, make_float2(f.x, f.y));
-    hi = add2(hi, make_float2(f.z, f.w));
+    a = add2(a, make_float2(f.x, f.y));
+    b = add2(b, make_float2(f.z, f.w));
   }
-  if constexpr (N == 4) {
-    v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
-  } else if constexpr (N == 2) {
-    v[0] = lo.x + hi.x; v[1] = lo.y + hi.y;
-  } else {
-    v[0] = (lo.x + lo.y) + (hi.x + hi.y);
-  }
+  v[0] = a.x + b.x;
+  v[1] = a.y + b.y;
 }
 
 // The same for four values and, where `fifth` is true, one more.  slot: 5 * 32
