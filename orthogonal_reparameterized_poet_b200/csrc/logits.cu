@@ -347,7 +347,7 @@ struct Pipe {
   float4 warp[2][8];
   int abort;
 };
-// from, to: warps that fill a buffer and that empty it.
+// from, to: warps that fill a buffer that is handed over, and that empty it.
 template <int NW>
 __device__ __forceinline__ void pipe_init(Pipe &P, int stages, int size, int from, int to, cg::cluster_group &cl) {
   if (threadIdx.x == 0) {
@@ -1722,9 +1722,9 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
 // to 4096 columns, whichever comes first.  Alternatives are selected from every
 // slice and merged, which costs more the more of both there are: their slices
 // stay above 16384 columns, and at most four and 256 / K share a row.  Measured
-// (us, 1 / 2 / 4 / 8 CTAs a row): 4 rows of 32000 without 4.8 / 4.7 / 4.2 / 4.3,
-// with 20 10.7 / 10.8 / 11.5 / 16.5; 4 of 128000 without 10.4 / 7.5 / 5.7 / 4.8,
-// with 20 22.5 / 16.6 / 14.5 / 17.9, with 128 23.5 / 21.2 / 22.6 / 40.9.  A slice
+// (us, 1 / 2 / 4 / 8 CTAs a row of four warps): 4 rows of 32000 without 4.8 / 4.7
+// / 4.2 / 4.3, with 20 10.7 / 10.8 / 11.5 / 16.5; 4 of 128000 without 10.4 / 7.5 /
+// 5.7 / 4.8, with 20 22.5 / 16.6 / 14.5 / 17.9, with 128 23.5 / 21.2 / 22.6 / 40.9.  A slice
 // has at most SLICE columns.
 int cluster_of(int64_t T, int V, int K = 0) {
   const int least = K ? 16384 : 4096, most = K ? std::max(1, std::min(4, 256 / K)) : MAX_CLUSTER;
@@ -1837,6 +1837,10 @@ poet_status run_logp(LogpArgs &a, cudaStream_t st) {
   // with 20 142 / 192, with 64 232 / 248; 4096 of 64000 with 20 117 / 127, with 64 173 / 161; 4096 of 128000 with
   // 64 232 / 223, without 172 / 170; 16384 of 32000 without 194 / 189; with two / eight: 16384 of 8000 with 20
   // 155 / 313.
+  // With a row an SM at most there is nothing to share and eight warps are the quickest (two or four / eight on the
+  // GPU, with 20: 4 rows of 8000 8.2 / 7.4, of 32000 10.6 / 9.4, of 128000 14.8 / 12.2; of 1000, where eight warps
+  // have no logits for every thread, 6.6 / 13.7).
+  if (a.K && a.T <= num_sms() && a.V >= 4096) return run_logp<T, 8>(a, cluster, st);
   if (a.V <= NARROW && a.K <= 32) return run_logp<T, 2>(a, cluster, st);
   if (a.K && (a.K <= 32 || (a.K <= 64 && int64_t(a.V) * int64_t(sizeof(T)) <= MEDIUM)))
     return run_logp<T, 4>(a, cluster, st);
