@@ -540,7 +540,12 @@ POET_API poet_status poet_token_logprobs_grad(const void *logits, int64_t ld, in
  *             q_r = max(0, 1 - sum q) is the teacher's mass on all other
  *             tokens and p_r the student's:
  *             loss = sum_k q_k (ln q_k - ln p_k) + q_r (ln q_r - ln p_r).
- *             What is left below 2^-23 per entry is rounding and counts as 0.
+ *             What is left below 2^-23 per entry is rounding and counts as 0,
+ *             and so does q_r where the row's entries list every token.
+ *             The outcomes may sum to more than 1 (scaled log probabilities,
+ *             a token listed twice) or, with every token listed, to less:
+ *             loss and gradient are those of the sums as they stand, at a listed
+ *             token scale (p_v (sum q + q_r) - q_v).
  * A value of -inf has q = 0.  A token listed twice counts with both values.
  * loss: device float[T].  dlogits (may be NULL; T x V, dtype, row stride ldd,
  * may be logits): the gradient of sum_t dloss[t] loss[t] (dloss: device

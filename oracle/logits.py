@@ -102,15 +102,17 @@ def distill(x, tokens, values, dloss=None, value_scale=1.0, tail=False, scale=1.
         qd = np.zeros(V)
         np.add.at(qd, tokens[t][use], q[use])
         g = (1.0 if dloss is None else dloss[t]) * scale
-        row, m = p[t] - qd, p[t] + qd
+        # every ln p of the loss takes p along with it, once for each part of the mass that the loss counts
+        mass = q.sum() + (rest if tail and not inside.all() else 0.0)
+        row, m = p[t] * mass - qd, p[t] * mass + qd
         if tail and not inside.all():
             pr = p[t][~inside].sum()
             if rest > 0:
                 with np.errstate(divide="ignore"):
                     loss[t] += rest * (np.log(rest) - np.log(pr))
             if pr > 0:
-                row = np.where(inside, row, p[t] / pr * (pr - rest))
-                m = np.where(inside, m, p[t] / pr * (pr + rest))
+                row = np.where(inside, row, p[t] / pr * (pr * mass - rest))
+                m = np.where(inside, m, p[t] / pr * (pr * mass + rest))
             else:
                 row, m = np.where(inside, row, 0.0), np.where(inside, m, 0.0)
         if np.all(np.isneginf(x[t])):

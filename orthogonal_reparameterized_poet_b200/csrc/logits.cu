@@ -1255,10 +1255,10 @@ struct Teacher {
   float sum[MAX_K];  // of a token's first entry: the q of all its entries
   int idx[MAX_K];    // -1: left out
   int first[MAX_K];  // whether no earlier entry has the same token
-  float rest;        // q_r
+  float rest;        // q_r where it counts: 0 with every token listed
+  float mass;        // sum q + q_r, the mass that the loss counts: 1 unless the values sum to more, or leave nothing outside
   float m, s;        // running sum of the student's logits at the distinct tokens
   int live;          // entries that count
-  int distinct;      // tokens among them
   // tail: the slice's vectors that the marks are of, and the marks of its ends
   int base, nv;
   unsigned head, behind;
@@ -1393,23 +1393,24 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
   if (lane == 0) {
     S.live = n;
     const float rest = 1.f - s;
-    S.rest = a.tail && !(rest < float(n) * 1.1920929e-7f) ? rest : 0.f;
+    S.rest = a.tail && distinct < a.V && !(rest < float(n) * 1.1920929e-7f) ? rest : 0.f;
+    S.mass = a.tail ? s + S.rest : 1.f;
     S.m = m;
     S.s = es;
-    S.distinct = distinct;
   }
   __syncwarp();
 }
 
 // Puts the teacher's tokens of the slice [lo, hi) right after the other
-// elements were written: (p - q) g.  All threads of the CTA that compute.
+// elements were written: (p (sum q + q_r) - q) g.  All threads of the CTA that
+// compute.
 template <typename T>
 __device__ __forceinline__ void write_teacher(const Teacher &S, const DistillArgs &a, T *out, int lo, int hi, float M,
                                               float logs, float g, int threads) {
   for (int k = threadIdx.x; k < a.K; k += threads)
     if (S.first[k] && S.idx[k] >= lo && S.idx[k] < hi) {
       const float p = S.x[k] == -INFINITY ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
-      out[S.idx[k]] = from_float<T>((p - S.sum[k]) * g);
+      out[S.idx[k]] = from_float<T>((p * S.mass - S.sum[k]) * g);
     }
 }
 
@@ -1422,8 +1423,8 @@ __device__ __forceinline__ Outside outside_of(const Teacher &S, int tail, float 
   if (tail) {
     if (ltail == -INFINITY) {  // no token there, or only masked ones
       o.f = 0.f;
-    } else {  // p_v (1 - q_r / p_r) = exp(z_v - ltail) (p_r - q_r)
-      o.f = ex2((ltail - logs) * LOG2E) - S.rest;
+    } else {  // p_v (sum q + q_r - q_r / p_r) = exp(z_v - ltail) (p_r (sum q + q_r) - q_r)
+      o.f = ex2((ltail - logs) * LOG2E) * S.mass - S.rest;
       o.L = ltail;
     }
   }
@@ -1592,7 +1593,7 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       if (tid == 0) {
-        if (a.tail && S.rest > 0.f && S.distinct < a.V)
+        if (S.rest > 0.f)
           l += S.rest * (logf(S.rest) - (empty ? -INFINITY : ltail - logs));
         a.loss[row] = bad ? NAN : l;
         if (a.saved)
