@@ -50,15 +50,43 @@ struct JointFwdArgs {
   float alpha, beta, eps;
 };
 
-// The sigmoid's exponential and reciprocal are the hardware's: their few units
-// in the last place are far below a bf16 output's rounding.
-__device__ __forceinline__ float sigmoid(float g) {
-  float e, r;
+// The sigmoid is r = 1 / (1 + e) with e = exp(-g), its slope e r^2: r (1 - r)
+// would lose its digits as the gate opens (r rounds to 1 from g = 17 on).  For
+// bf16 operands the exponential and the reciprocal are the hardware's: their
+// relative error, about 2^-23 (2 + |g|), stays below the rounding of a bf16
+// result, 2^-9, for every gate whose slope is not 0 in float.  For float operands
+// they are CUDA's functions, to a unit or two in the last place.
+template <typename T>
+__device__ __forceinline__ float exp_minus(float g) {
+  if constexpr (sizeof(T) == 4) return expf(-g);
+  float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  return e;
+}
+template <typename T>
+__device__ __forceinline__ float sigmoid_of(float e) {
+  if constexpr (sizeof(T) == 4) return __frcp_rn(1.f + e);
+  float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
-__device__ __forceinline__ float act_of(float g, int sig) { return sig ? sigmoid(g) : g; }
+template <typename T>
+__device__ __forceinline__ float2 exp_minus(float2 g) {
+  return make_float2(exp_minus<T>(g.x), exp_minus<T>(g.y));
+}
+template <typename T>
+__device__ __forceinline__ float2 sigmoid_of(float2 e) {
+  return make_float2(sigmoid_of<T>(e.x), sigmoid_of<T>(e.y));
+}
+// e r is 1 - r, between 0 and 1; infinity times 0, of a closed gate, saturates to
+// 0 (a NaN's slope is still one: r is).
+__device__ __forceinline__ float2 slope_of(float2 e, float2 r) {
+  return mul2(make_float2(__saturatef(e.x * r.x), __saturatef(e.y * r.y)), r);
+}
+template <typename T>
+__device__ __forceinline__ float act_of(float g, int sig) {
+  return sig ? sigmoid_of<T>(exp_minus<T>(g)) : g;
+}
 
 // A thread's own ring of the rows to come.  With S stages every thread copies
 // its 16 bytes of each operand of row r + S - 1 into its own place in shared
@@ -307,7 +335,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
       if (r != r0) ++grow;
       gnext = (grow + 1) * a.gate_rows;
       if (!SHARED) {
-        gval = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
+        gval = act_of<T>(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
       } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
         branch_gains();
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          wq[p] = mul2(wq[p], make_float2(act_of(gv[p].x, a.gate_sigmoid), act_of(gv[p].y, a.gate_sigmoid)));
+          wq[p] = mul2(wq[p], make_float2(act_of<T>(gv[p].x, a.gate_sigmoid), act_of<T>(gv[p].y, a.gate_sigmoid)));
       }
     }
     float2 x[NP];
@@ -336,7 +364,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
         vg.get(gv);
         if (a.gate_sigmoid) {
 #pragma unroll
-          for (int p = 0; p < NP; ++p) gv[p] = make_float2(sigmoid(gv[p].x), sigmoid(gv[p].y));
+          for (int p = 0; p < NP; ++p) gv[p] = sigmoid_of<T>(exp_minus<T>(gv[p]));
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) q[p] = mul2(q[p], gv[p]);
@@ -544,8 +572,12 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
       }
       gnext = (grow + 1) * a.gate_rows;
       if (!SHARED) {
-        ga_row = act_of(to_float(gate[grow * a.ldg]), a.gate_sigmoid);
-        sl_row = a.gate_sigmoid ? ga_row * (1.f - ga_row) : 1.f;
+        ga_row = to_float(gate[grow * a.ldg]);
+        if (a.gate_sigmoid) {
+          const float2 e = both(exp_minus<T>(ga_row)), r = both(sigmoid_of<T>(e.x));
+          ga_row = r.x;
+          sl_row = slope_of(e, r).x;
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -602,10 +634,14 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
       gq.get(wq);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        float2 ga = both(ga_row);
+        float2 ga = both(ga_row), sl = both(1.f);
         if (EACH || SHARED) {
           ga = dg[p];
-          if (a.gate_sigmoid) ga = make_float2(sigmoid(ga.x), sigmoid(ga.y));
+          if (a.gate_sigmoid) {
+            const float2 e = exp_minus<T>(ga);
+            ga = sigmoid_of<T>(e);
+            sl = slope_of(e, ga);
+          }
         }
         const float2 da = mul2(t[p], beta), dp = mul2(da, ga);
         q[p] = mul2(q[p], both(ro));
@@ -615,7 +651,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
         w0 = fma2(dp, z, w0);
         if (EACH || SHARED) {
           dg[p] = mul2(da, z);
-          if (a.gate_sigmoid) dg[p] = mul2(dg[p], fma2(ga, mul2(ga, both(-1.f)), ga));
+          if (a.gate_sigmoid) dg[p] = mul2(dg[p], sl);
           if (SHARED) ag[p] = add2(ag[p], dg[p]);
         } else {
           w1 = fma2(da, z, w1);

@@ -1,0 +1,56 @@
+"""The joint at the edges of what it accepts, against the float64 oracle
+(oracle/joint.py), with the bounds of tests/test_gpu_joint.py."""
+import numpy as np
+import pytest
+
+from oracle import joint as J
+from tests.test_gpu_joint import _case, _close, _np, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# Beside the operators' 64 half steps, those of the sigmoid: of its exponent of at most 20 log2(e) = 28.9, 12 for its
+# rounding, 10 for the constant's and 4 for the exponential; of the sum, the reciprocal and the products 9 more.
+SIGMOID = 40
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,d", [(41, 64), (300, 136), (5, 2560), (3, 4600), (7, 1377), (2, 16384)])
+@pytest.mark.parametrize("gate,rows", [("channel", 1), ("channel", 3), ("channel", 1 << 40), ("row", 1), ("row", 4)])
+def test_gates_wide_open_and_closed(torch, T, d, gate, rows, dtype):  # noqa: F811
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    c = _case(torch, T, d, getattr(torch, dtype), gate, True, rows)
+    g = c["gate"]
+    g.copy_(torch.linspace(-20, 20, g.numel(), device="cuda").reshape(g.shape))
+    want_h, want_n, mh, mn = J.forward(_np(c["o"]), _np(c["h"]), _np(g), **c["ref"])
+    h, n = poet.joint_forward(c["o"], c["h"], g, **c["kw"])
+    _close(torch, h, want_h, mh, 64 + SIGMOID, "h'")
+    _close(torch, n, want_n, mn, 64 + SIGMOID, "n")
+    want = J.backward(_np(c["o"]), _np(h), _np(g), _np(c["dh_out"]), _np(c["dn"]), **c["ref"])
+    got = poet.joint_backward(c["o"], h, g, c["dh_out"], c["dn"], **c["kw"])
+    poet.poet_sync_status()
+    for name, t in zip(("dh", "do", "dgate", "dw_post", "dw_pre"), got):
+        steps = 64 + SIGMOID + (T if name.startswith("dw") or name == "dgate" else 0)
+        if name == "dgate" and g.dim() == 1:
+            steps += 64
+        _close(torch, t, want[name][0], want[name][1], steps, name)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_gates_beyond_the_exponential(torch, dtype):  # noqa: F811
+    """Gates whose exponentials leave a float's range: open is 1 and closed is 0, both with slope 0; a NaN stays."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    c = _case(torch, 6, 64, getattr(torch, dtype), "channel", True, 1, alpha=0.0)
+    g = c["gate"]
+    for i, v in enumerate((float("-inf"), -3e38, -150.0, 150.0, 3e38, float("inf"))):
+        g[i] = v
+    h, n = poet.joint_forward(c["o"], c["h"], g, **c["kw"])
+    assert torch.equal(h[:3], torch.zeros_like(h[:3])) and (h[3:] != 0).all() and torch.isfinite(h).all()
+    got = poet.joint_backward(c["o"], c["h"], g, c["dh_out"], c["dn"], **c["kw"])
+    # the slopes beyond 88 are below 2^-126 and the other factors below 2^20
+    assert (got[2].abs() <= 2.0 ** -100).all() and all(torch.isfinite(t).all() for t in got)
+    g[2, 5] = float("nan")
+    got = poet.joint_backward(c["o"], c["h"], g, c["dh_out"], c["dn"], **c["kw"])
+    assert torch.isnan(got[2][2, 5]) and torch.isfinite(got[2][:2]).all()
