@@ -1402,14 +1402,14 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
 }
 
 // Puts the teacher's tokens of the slice [lo, hi) right after the other
-// elements were written: (p (sum q + q_r) - q) g.  All threads of the CTA that
-// compute.
+// elements were written: (p (sum q + q_r) - q) g, all NaN in a row whose M is.
+// All threads of the CTA that compute.
 template <typename T>
 __device__ __forceinline__ void write_teacher(const Teacher &S, const DistillArgs &a, T *out, int lo, int hi, float M,
                                               float logs, float g, int threads) {
   for (int k = threadIdx.x; k < a.K; k += threads)
     if (S.first[k] && S.idx[k] >= lo && S.idx[k] < hi) {
-      const float p = S.x[k] == -INFINITY ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
+      const float p = S.x[k] == -INFINITY && M == M ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
       out[S.idx[k]] = from_float<T>((p * S.mass - S.sum[k]) * g);
     }
 }
