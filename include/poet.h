@@ -489,10 +489,13 @@ POET_API poet_status poet_joint_backward(const poet_joint *J, const void *o, int
  *    1 <= V <= 2097152.  Only the V columns of a row are read.  The
  *    distribution of a row is p_v = softmax(scale x_v), scale > 0 (an inverse
  *    temperature).
- *  - A logit of -inf is a masked token: its probability and its gradient are 0
- *    and it is never listed as an alternative.  A row of nothing but -inf has
- *    log probability -inf, entropy 0 and a gradient of 0.  A row with a NaN or
- *    +inf logit gives NaN (and no alternatives) for that row alone.
+ *  - A logit of -inf is a masked token: its probability is 0, it is never
+ *    listed as an alternative, and its gradient is 0 unless it is the given
+ *    token or one of the teacher's.  There the log probability is -inf, the
+ *    loss +inf, and the gradients are the formulas' with p = 0: dlogp scale,
+ *    -q dloss scale.  A row of nothing but -inf has log probability -inf,
+ *    entropy 0 and a gradient of 0.  A row with a NaN or +inf logit gives NaN
+ *    (and no alternatives) for that row alone.
  *  - tokens: device int32[T].  A negative token marks a row to leave out
  *    (padding): its logits are not read, its log probability, entropy and
  *    gradient are 0 and its alternatives empty.  A token >= V does the same and
