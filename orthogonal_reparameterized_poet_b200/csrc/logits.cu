@@ -47,6 +47,9 @@ constexpr int CAND = 1536;     // candidates kept at once by the selection: 192 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -1e30f;
 
+// scale log2(e), finite: an infinite one would make NaN of a difference of 0.
+__device__ __forceinline__ float log2_scale(float scale) { return fminf(scale * LOG2E, 3.4028234e38f); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -919,7 +922,7 @@ __device__ __forceinline__ void logp_rows(const LogpArgs &a, Pipe &P, Select &S,
                                           int rank, int size, int64_t first, int64_t step) {
   constexpr int G = NW * 32, SV = G * U;
   const int tid = threadIdx.x;
-  const float c = a.scale * LOG2E;
+  const float c = log2_scale(a.scale);
   Spot at;
   uint32_t round = 0;  // rows handed over
   int token = a.tokens && first < a.T ? a.tokens[first] : 0;
@@ -981,7 +984,7 @@ __device__ __forceinline__ void finish_rows(const LogpArgs &a, Pipe &P, Select &
                                             int tid) {
   constexpr int NS = select_warps<NW>(), NN = (TOP ? NS : 1) * 32;
   const unsigned K = unsigned(a.K);
-  const float c = a.scale * LOG2E;
+  const float c = log2_scale(a.scale);
   uint32_t round = 0;
   int token = a.tokens && first < a.T ? a.tokens[first] : 0;
   for (int64_t row = first; row < a.T; row += step) {
@@ -1206,7 +1209,7 @@ __global__ void __launch_bounds__(NT) logp_grad_kernel(const LogpGradArgs a) {
     zero_slice<T, NT>(out, sl.lo, sl.hi);
     return;
   }
-  const float c = a.scale * LOG2E, L = sv.y * LOG2E;
+  const float c = log2_scale(a.scale), L = sv.y * LOG2E;
   const float gl = a.dlogp ? a.dlogp[row] : 0.f, gh = a.dentropy ? a.dentropy[row] : 0.f;
   const bool mine = a.dlogp && token >= sl.lo && token < sl.hi;
   const float xt = mine ? to_float(x[token]) : 0.f;
@@ -1289,7 +1292,7 @@ struct Entries {
 __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, const Entries &e, bool report) {
   constexpr int Q = Entries::Q;
   const int lane = threadIdx.x & 31;
-  const float c = a.scale * LOG2E;
+  const float c = log2_scale(a.scale);
   int t[Q];
   float lq[Q], xs[Q], q[Q];
   float mx = -INFINITY;
@@ -1409,7 +1412,7 @@ __device__ __forceinline__ void write_teacher(const Teacher &S, const DistillArg
                                               float logs, float g, int threads) {
   for (int k = threadIdx.x; k < a.K; k += threads)
     if (S.first[k] && S.idx[k] >= lo && S.idx[k] < hi) {
-      const float p = S.x[k] == -INFINITY && M == M ? 0.f : ex2(fmaf(S.x[k] - M, a.scale * LOG2E, -logs * LOG2E));
+      const float p = S.x[k] == -INFINITY && M == M ? 0.f : ex2(fmaf(S.x[k] - M, log2_scale(a.scale), -logs * LOG2E));
       out[S.idx[k]] = from_float<T>((p * S.mass - S.sum[k]) * g);
     }
 }
@@ -1519,7 +1522,7 @@ __device__ __forceinline__ void distill_rows(const DistillArgs &a, Pipe &P, cons
                                              int rank, int size, int64_t first, int64_t step) {
   constexpr int G = NW * 32, SV = G * U, E = Vec<T>::E;
   const int tid = threadIdx.x;
-  const float c = a.scale * LOG2E;
+  const float c = log2_scale(a.scale);
   Spot at;
   int par = 0;
   int64_t n = 0;
@@ -1707,7 +1710,7 @@ __global__ void __launch_bounds__(NT) distill_grad_kernel(const DistillArgs a) {
     zero_slice<T, NT>(out, sl.lo, sl.hi);
     return;
   }
-  const float c = a.scale * LOG2E;
+  const float c = log2_scale(a.scale);
   const float g = (a.dloss ? a.dloss[row] : 1.f) * a.scale;
   const Outside o = outside_of(S, a.tail, sv.y, sv.w);
   const float A = o.f * g, L = o.L * LOG2E, M = sv.x;

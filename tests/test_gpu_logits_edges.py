@@ -1,8 +1,11 @@
 """Operators on logits at the edges of what they accept, against the float64
 oracle (oracle/logits.py), with the bounds of tests/test_gpu_logits.py."""
+import numpy as np
 import pytest
 
-from tests.test_gpu_logits import INF, _make, _teacher_case, torch  # noqa: F401
+from oracle import logits as G
+from tests.test_gpu_logits import (INF, U, _check_distill, _check_logprobs, _gap, _make, _np, _steps, _teacher_case,
+                                   _within, torch)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +55,32 @@ def test_masked_targets(torch, dtype):  # noqa: F811
     assert loss[0] == INF and loss[2] == INF and torch.isfinite(loss[1])
     for g in (d, again):  # q = 1/2
         assert g[0, 150] == -0.5 * 0.75 * 0.5 and g[2, 399] == -0.5 * 2.0 * 0.5 and (g[masked] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V", [5, 3000, 40000])
+@pytest.mark.parametrize("scale", [1e-37, 1e30, 2e38, 3.4e38])
+def test_extreme_scales(torch, V, scale, dtype):  # noqa: F811
+    """Up to the largest float: all the mass on the largest logits."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    x, r = _make(torch, 4, V, getattr(torch, dtype))
+    x[:, 2] = 30.0
+    x[1, 4] = 30.0  # two of them
+    if V > 5:
+        x[2, 7] = -INF
+    tokens = np.array([2, 4, 3, 0])
+    tk, saved = _check_logprobs(torch, x, tokens, 3, scale)
+    dl, de = (r.standard_normal(4).astype(np.float32) * np.float32(0.5 / scale) for _ in range(2))
+    got = poet.token_logprobs_grad(x, tk, saved, torch.from_numpy(dl).cuda(), torch.from_numpy(de).cuda(), scale=scale)
+    s = float(np.float32(scale))
+    want, mag = G.token_logprobs_grad(_np(x), tokens, dl.astype(float), de.astype(float), s)
+    near = np.minimum(_gap(_np(x), s), 200)  # beyond, a probability is 0 in float
+    half = torch.finfo(x.dtype).eps / 2
+    _within("dlogits", _np(got), want, half * np.abs(want) * 1.01 + (2 * _steps(V) + 6 * (near + np.log(V)) + 16) * U * mag
+            + 1e-36)
+    tokens, values = _teacher_case(r, 4, V, 3, False)
+    tokens[:, 0] = 2
+    if V > 5:
+        tokens[2][tokens[2] == 7] = 9
+    _check_distill(torch, x, tokens, values, r, False, scale, weights=False)
