@@ -1219,13 +1219,15 @@ __global__ void __launch_bounds__(NT) logp_grad_kernel(const LogpGradArgs a) {
   float k;
   if (a.dentropy) {
     // -gl p - gh p (ln p + H) = p (B + C log2 p)
+    // where p is 0 in float (below 2^-126), ln p stays small enough for its product with a large weight
     const float B = A - gh * a.scale * sv.z, C = -gh * a.scale * LN2;
+    constexpr float NONE = -200.f;
     map_slice(x, out, sl, [=](int, float v) {
       const float d = fmaf(v - M, c, -L);
-      return ex2(d) * fmaf(C, fmaxf(d, LOWEST), B);
+      return ex2(d) * fmaf(C, fmaxf(d, NONE), B);
     });
     const float d = fmaf(xt - M, c, -L);
-    k = ex2(d) * fmaf(C, fmaxf(d, LOWEST), B);
+    k = ex2(d) * fmaf(C, fmaxf(d, NONE), B);
   } else {
     map_slice(x, out, sl, [=](int, float v) { return A * ex2(fmaf(v - M, c, -L)); });
     k = A * ex2(fmaf(xt - M, c, -L));

@@ -84,3 +84,25 @@ def test_extreme_scales(torch, V, scale, dtype):  # noqa: F811
     if V > 5:
         tokens[2][tokens[2] == 7] = 9
     _check_distill(torch, x, tokens, values, r, False, scale, weights=False)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("weight", [1.0, 1e9, 1e30])
+def test_large_weights_of_the_entropy(torch, weight, dtype):  # noqa: F811
+    """Probabilities of 0 (masked logits, far ones) have a gradient of 0, whatever the entropy's weight."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    V = 2000
+    x, r = _make(torch, 5, V, getattr(torch, dtype), masked=0.3)
+    x[0, ::2] = torch.finfo(x.dtype).min
+    x[:, 11] = -500.0
+    tk = torch.from_numpy(r.integers(0, V, 5).astype(np.int32)).cuda()
+    saved = poet.token_logprobs(x, tk)[4]
+    de = (r.standard_normal(5) * weight).astype(np.float32)
+    got = poet.token_logprobs_grad(x, tk, saved, None, torch.from_numpy(de).cuda())
+    want, mag = G.token_logprobs_grad(_np(x), tk.cpu().numpy(), None, de.astype(float), 1.0)
+    half = torch.finfo(x.dtype).eps / 2
+    near = np.minimum(_gap(_np(x), 1.0), 200)
+    _within("dlogits", _np(got), want, half * np.abs(want) * 1.01 + (2 * _steps(V) + 6 * (near + np.log(V)) + 16) * U * mag
+            + 1e-36 * weight)
+    assert (got[torch.isneginf(x)] == 0).all()
