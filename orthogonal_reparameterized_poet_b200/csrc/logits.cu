@@ -1828,6 +1828,8 @@ poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
   if (a.K) extra = sizeof(Select) + (cluster > 1 ? size_t(2) * cluster * a.K * 8 : 0) + size_t(2) * a.key_floats * 4;
   const Spread s = spread<NW>(a.T, cluster, extra, 2048, per_sm<NW>(!a.K));
   a.stages = s.stages;
+  // A caller that wants neither the entropy nor saved (which holds it) does without its sum.  Measured with / without
+  // (us on the GPU, bf16): 16384 rows of 32000 191 / 180, 4096 of 128000 with 64 alternatives 223 / 210.
   const bool ent = a.entropy || a.saved;
   if (a.K)
     return ent ? launch_rows<logp_kernel<T, NW, true, true>>(a, s, logp_threads<NW, true>(), st, "logprobs")

@@ -106,3 +106,42 @@ def test_large_weights_of_the_entropy(torch, weight, dtype):  # noqa: F811
     _within("dlogits", _np(got), want, half * np.abs(want) * 1.01 + (2 * _steps(V) + 6 * (near + np.log(V)) + 16) * U * mag
             + 1e-36 * weight)
     assert (got[torch.isneginf(x)] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,V,K", [(3, 7, 0), (5, 1000, 0), (400, 3001, 0), (2, 50257, 0), (1, 300000, 0), (300, 16000, 0),
+                                   (3, 40, 5), (5, 1000, 20), (4, 32000, 20), (400, 3000, 128), (300, 20000, 40), (1, 128000, 9)])
+@pytest.mark.parametrize("kind", ["plain", "masked", "far"])
+def test_without_entropy(torch, T, V, K, kind, dtype):  # noqa: F811
+    """Through the C ABI with neither the entropy nor what the backward reads: a sum of its own."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    t = getattr(torch, dtype)
+    x, r = _make(torch, T, V, t, masked=0.4 if kind == "masked" else 0.0, seed=K)
+    if kind == "masked":
+        x[0] = -INF
+        if T > 1:
+            x[1, ::3] = torch.finfo(t).min
+    elif kind == "far":  # sums against a base that a fused operation would not do for
+        x += torch.tensor(3.0e6 if t == torch.float32 else 2.0 ** 30, device="cuda").to(t)
+    tokens = r.integers(0, V, T)
+    tk = torch.from_numpy(tokens.astype(np.int32)).cuda()
+    logp = torch.empty(T, device="cuda")
+    top = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    topl = torch.empty(T, K, device="cuda")
+    at = lambda v: v.data_ptr() if K else None  # noqa: E731
+    st = torch.cuda.current_stream().cuda_stream
+    status = poet.lib().poet_token_logprobs(x.data_ptr(), V, poet.BF16 if t == torch.bfloat16 else poet.F32, T, V, 0.9,
+                                            tk.data_ptr(), K, logp.data_ptr(), None, at(top), at(topl), None, st)
+    assert status == poet.OK
+    poet.poet_sync_status()
+    X, s = _np(x), float(np.float32(0.9))
+    want, _, want_top, want_topl = G.token_logprobs(X, tokens, K, s)
+    gap, N, lse = _gap(X, s), _steps(V), np.log(V) + 1
+    _within("logp", _np(logp), want, (N + 3 * gap[np.arange(T), tokens] + 2 * np.abs(want) + 2 * lse) * U)
+    if K:
+        assert np.array_equal(top.cpu().numpy(), want_top)
+        finite = np.isfinite(want_topl)
+        g = np.take_along_axis(gap, np.maximum(want_top, 0).astype(np.int64), 1)
+        with np.errstate(invalid="ignore"):
+            _within("top_logp", _np(topl), want_topl, (N + 3 * g + 2 * np.where(finite, np.abs(want_topl), 0) + 2 * lse) * U)
