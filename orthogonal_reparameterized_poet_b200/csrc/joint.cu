@@ -952,7 +952,7 @@ poet_status poet_joint_forward(const poet_joint *J, const void *o, int64_t ldo, 
   a.rows_per_group = (T + fill - 1) / fill;
   const int64_t groups = (T + a.rows_per_group - 1) / a.rows_per_group;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t G = (T + J->gate_rows - 1) / J->gate_rows;
+  const int64_t G = T / J->gate_rows + (T % J->gate_rows ? 1 : 0);
   const double gate_elems = a.gate_kind == POET_GATE_CHANNEL ? double(G) * d : a.gate_kind == POET_GATE_ROW ? double(G) : 0.0;
   TraceScope ts("joint", 14.0 * double(T) * d,
                 (double(T) * d * ((o ? 3 : 1) + (n ? 1 : 0)) + gate_elems) * double(esize(dt)), st);
@@ -1048,7 +1048,7 @@ poet_status poet_joint_backward(const poet_joint *J, const void *o, int64_t ldo,
   a.part_post = dw_post ? reinterpret_cast<float *>(wb) : nullptr;
   a.part_pre = dw_pre ? reinterpret_cast<float *>(wb + part) : nullptr;
   a.part_gate = reinterpret_cast<float *>(wb + 2 * part);
-  const int64_t G = (T + J->gate_rows - 1) / J->gate_rows;
+  const int64_t G = T / J->gate_rows + (T % J->gate_rows ? 1 : 0);
   const double gate_elems = channel ? 2.0 * double(G) * d : a.gate_kind == POET_GATE_ROW ? 2.0 * double(G) : 0.0;
   const int passes = 1 + (o ? 2 : 0) + (dn ? 2 : 0) + (dh_out ? 1 : 0);
   TraceScope ts("joint_bwd", 30.0 * double(T) * d, (double(T) * d * passes + gate_elems) * double(esize(dt)), st);

@@ -54,3 +54,24 @@ def test_gates_beyond_the_exponential(torch, dtype):  # noqa: F811
     g[2, 5] = float("nan")
     got = poet.joint_backward(c["o"], c["h"], g, c["dh_out"], c["dn"], **c["kw"])
     assert torch.isnan(got[2][2, 5]) and torch.isfinite(got[2][:2]).all()
+
+
+@pytest.mark.parametrize("gate", ["channel", "row"])
+def test_one_gate_for_any_number_of_tokens(torch, gate):  # noqa: F811
+    """gate_rows up to the largest integer: the same bits as with the number of tokens, and the same bytes recorded."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    got = []
+    for rows in (37, 2**63 - 1):
+        c = _case(torch, 37, 128, torch.float32, gate, True, 37)
+        c["kw"]["gate_rows"] = rows
+        poet.poet_trace_enable(True)
+        try:
+            h, n = poet.joint_forward(c["o"], c["h"], c["gate"], **c["kw"])
+            out = [h, n, *poet.joint_backward(c["o"], h, c["gate"], c["dh_out"], c["dn"], **c["kw"])]
+            rec = {k: (v["launches"], v["bytes"]) for k, v in poet.poet_trace_read().items()}
+        finally:
+            poet.poet_trace_enable(False)
+        got.append((out, rec))
+    assert all(torch.equal(a, b) for a, b in zip(got[0][0], got[1][0]))
+    assert got[0][1] == got[1][1] and got[0][1]["joint"][0] == 1
