@@ -751,8 +751,16 @@ _MAXI32 = 2**31 - 1
 _F32, _I32 = torch.float32, torch.int32
 
 
+def _fits(x, name, bits):
+    """Refuses an integer that the C ABI would cut to `bits` bits."""
+    if not -(1 << bits - 1) <= x < 1 << bits - 1:
+        raise ValueError(f"{name} {x} does not fit {bits} bits")
+
+
 def _joint(h, o, gate, w_post, w_pre, post_norm, gate_act, gate_rows, alpha, beta, eps):
     """The poet_joint of these options, with the addresses and strides of o, h and the gate."""
+    _fits(gate_act, "gate_act", 32)
+    _fits(gate_rows, "gate_rows", 64)
     shape = h.shape
     if len(shape) != 2:
         raise ValueError("h must be 2-D (tokens x width)")
@@ -824,6 +832,10 @@ def joint_forward(o, h, gate=None, *, w_post=None, w_pre=None, post_norm=True, p
 
 def joint_workspace_bytes(T, d, dtype, gate=GATE_NONE, gate_rows=1):
     """Bytes of workspace joint_backward needs (dtype: F32 or BF16)."""
+    for name, x in (("d", d), ("dtype", dtype), ("gate", gate)):
+        _fits(x, name, 32)
+    _fits(T, "T", 64)
+    _fits(gate_rows, "gate_rows", 64)
     J = poet_joint(d, dtype, 0, gate, 0, 0, gate_rows, 1.0, 1.0, 1.0, None, None)
     return lib().poet_joint_workspace_bytes(ctypes.byref(J), T)
 
@@ -940,6 +952,7 @@ def token_logprobs(logits, tokens=None, *, topk=0, scale=1.0, entropy=True, save
         r = _native().token_logprobs(logits, tokens, topk, scale, entropy)
         if r is not None:
             return r if type(r) is tuple else _check(r)
+    _fits(topk, "topk", 32)
     dev, dt, T, V, px, ld = _logits(logits)
     pt = _per_row(tokens, "tokens", T, _I32, dev)
     st = _stream_on(stream, dev)
