@@ -904,6 +904,8 @@ def joint_backward(o, h_out, gate, dh_out, dn, *, w_post=None, w_pre=None, post_
         ws = _new((lib().poet_joint_workspace_bytes(J_at, T) or 1,), torch.uint8, dev, stream)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}, not on cuda:{dev}")
+    elif not ws.is_contiguous():  # its bytes are not all there, or not all its own
+        raise ValueError("ws must be contiguous")
     _check(lib().poet_joint_backward(J_at, po, ldo, ph, ldh, pg, ldg, pd, ldd, pn, ldn, T, pdh, lddh, pdo, lddo, pdg,
                                      lddg, pwq, pwn, ws.data_ptr(), ws.nbytes, st))
     return dh, d_o, dgate, dw_post, dw_pre
