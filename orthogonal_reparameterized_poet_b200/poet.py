@@ -699,7 +699,8 @@ def _dtype_of(t, what):
 
 def _plain(t, shape, dtype, device):
     """Whether t is a contiguous tensor of this shape and type on that device: what nearly every operand is."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous() and
+            not t.is_neg())
 
 
 def _operand(t, name, shape, dtype, device, rows=True):
@@ -712,6 +713,8 @@ def _operand(t, name, shape, dtype, device, rows=True):
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.is_neg():  # its memory holds the values of the other sign
+        raise ValueError(f"{name} is a negated view; pass {name}.resolve_neg()")
     if rows and t.dim() == 2:
         if t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"the rows of {name} must be contiguous (stride(1) == 1)")
