@@ -1,11 +1,13 @@
-"""Build libpoet.so in-tree for sm_100a with nvcc (no JIT, no torch extension).
+"""Build libpoet.so in-tree for sm_100a with nvcc (no JIT; libpoet.so does not need torch).
 
     python -m orthogonal_reparameterized_poet_b200.build [--force]
 
 Each .cu under csrc/ is compiled to an object under _build/ (in parallel),
 then linked into orthogonal_reparameterized_poet_b200/libpoet.so.  Objects
 are rebuilt when their source, a header, or this file is newer.  csrc/binding.cpp
-becomes _binding.so beside it (the host compiler, torch's headers).
+becomes _binding.<python>.torch-<version>.so beside it (the host compiler, torch's
+headers), the compiled binding of this interpreter and this torch.  Where it cannot
+be compiled the build warns and goes on: every call works through ctypes too.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpoet.so")
-BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -50,10 +52,18 @@ def _compile(src, force):
     return obj
 
 
+def binding_path() -> str:
+    """Where the compiled binding for this interpreter and this torch lies: it uses their C++ interfaces, so one
+    that was built for others must not be loaded."""
+    import torch
+
+    return os.path.join(PKG, f"_binding.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
+
+
 def _binding(force):
     """The binding of the operators on torch tensors, linked against libpoet.so beside it."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not (force or _stale(BINDING, [src] + _headers())):
+    src, path = os.path.join(CSRC, "binding.cpp"), binding_path()
+    if not (force or _stale(path, [src] + _headers())):
         return
     import sysconfig
 
@@ -65,11 +75,21 @@ def _binding(force):
     include = cpp_extension.include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in include], src,
-           "-o", BINDING, f"-L{PKG}", "-l:libpoet.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda",
+           "-o", path, f"-L{PKG}", "-l:libpoet.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"the binding failed to compile:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{r.stdout}\n{r.stderr}")
+    for other in glob.glob(os.path.join(PKG, "_binding*.so")):  # of another torch or interpreter
+        if other != path:
+            os.remove(other)
+
+
+def _binding_if_possible(force):
+    try:
+        _binding(force)
+    except (OSError, ImportError, RuntimeError) as e:
+        warnings.warn(f"the compiled binding could not be built; calls go through ctypes:\n{e}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -82,7 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    _binding(force)
+    _binding_if_possible(force)
     if verbose:
         print(LIB)
     return LIB

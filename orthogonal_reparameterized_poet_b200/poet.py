@@ -10,8 +10,11 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
+
+from .build import binding_path
 
 F32, BF16 = 0, 1
 BS, FS = 0, 1
@@ -22,9 +25,7 @@ OK, EINVAL, ECUDA, ETIMEOUT, ENOMEM_WS, EBOUNDS = 0, 1, 2, 3, 4, 5
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpoet.so")
 _lib = None
-# the common call of the operators around the blocks (csrc/binding.cpp)
-_BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
-_binding = None
+_binding = None  # the common call of the operators around the blocks (csrc/binding.cpp)
 
 
 class PoetError(RuntimeError):
@@ -187,17 +188,30 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+class _NoBinding:
+    """In place of the compiled binding where there is none: leaves every call to the ctypes path."""
+
+    def _leave(*args):
+        return None
+
+    joint_forward = joint_backward = token_logprobs = token_logprobs_grad = distill_topk = distill_topk_grad = \
+        staticmethod(_leave)
+
+
 def _native():
-    """The compiled binding of the operators around the blocks (raises if it is not built)."""
+    """The compiled binding of the operators around the blocks, if it is built for this torch."""
     global _binding
     if _binding is None:
         lib()
-        if not os.path.exists(_BINDING_PATH):
-            raise RuntimeError(f"_binding.so not built at {_BINDING_PATH}; run "
-                               "`python -m orthogonal_reparameterized_poet_b200.build`")
-        spec = importlib.util.spec_from_file_location("_binding", _BINDING_PATH)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
+        path = binding_path()
+        try:
+            spec = importlib.util.spec_from_file_location("_binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except ImportError as e:
+            warnings.warn(f"no compiled binding at {path} ({e}): calls go through ctypes, at about twice the host "
+                          "time; run `python -m orthogonal_reparameterized_poet_b200.build`")
+            module = _NoBinding
         _binding = module
     return _binding
 
