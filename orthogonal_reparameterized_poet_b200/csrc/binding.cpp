@@ -80,6 +80,18 @@ PyObject *wrap(const std::optional<Tensor> (&t)[N]) {
   }
   return r;
 }
+// Runs f without the interpreter's lock: other Python threads run while this one
+// allocates and launches, which may both wait for the GPU.  f touches no object of
+// the interpreter's; the caller's frame holds the tensors that it reads.
+template <typename F>
+poet_status unlocked(F f) {
+  struct Lock {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
+}
+
 PyObject *status(poet_status s) { return PyLong_FromLong(long(s)); }
 const Tensor *given(const std::optional<Tensor> &t) { return t ? &*t : nullptr; }
 
@@ -165,10 +177,12 @@ PyObject *joint_forward(PyObject *, Args a, Py_ssize_t n) {
     if (!j.take(a[0], a[1], a[2], a[3], a[4], a + 5)) Py_RETURN_NONE;
     const bool pre = PyObject_IsTrue(a[11]) == 1;
     std::optional<Tensor> out[2];
-    out[0] = fresh({j.T, j.d}, j.type, *j.h);
-    if (pre) out[1] = fresh({j.T, j.d}, j.type, *j.h);
-    const poet_status s = poet_joint_forward(&j.J, at_(j.o), j.d, at_(j.h), j.d, at_(j.gate), j.ldg, j.T, at_(given(out[0])),
-                                             j.d, at_(given(out[1])), j.d, stream_of(j.dev));
+    const poet_status s = unlocked([&] {
+      out[0] = fresh({j.T, j.d}, j.type, *j.h);
+      if (pre) out[1] = fresh({j.T, j.d}, j.type, *j.h);
+      return poet_joint_forward(&j.J, at_(j.o), j.d, at_(j.h), j.d, at_(j.gate), j.ldg, j.T, at_(given(out[0])), j.d,
+                                at_(given(out[1])), j.d, stream_of(j.dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
@@ -184,17 +198,19 @@ PyObject *joint_backward(PyObject *, Args a, Py_ssize_t n) {
         (!dn && j.w_pre))
       Py_RETURN_NONE;
     std::optional<Tensor> out[5];  // dh, d_o, dgate, dw_post, dw_pre
-    out[0] = fresh({j.T, j.d}, j.type, *j.h);
-    out[1] = fresh({j.T, j.d}, j.type, *j.h);
-    if (j.gate) out[2] = fresh(j.gate->sizes(), j.type, *j.h);
-    if (j.w_post) out[3] = fresh({j.d}, at::kFloat, *j.h);
-    if (j.w_pre) out[4] = fresh({j.d}, at::kFloat, *j.h);
-    const size_t bytes = poet_joint_workspace_bytes(&j.J, j.T);
-    const Tensor ws = fresh({int64_t(bytes ? bytes : 1)}, at::kByte, *j.h);
-    const poet_status s = poet_joint_backward(
-        &j.J, at_(j.o), j.d, at_(j.h), j.d, at_(j.gate), j.ldg, at_(dh_out), j.d, at_(dn), j.d, j.T, at_(given(out[0])), j.d,
-        at_(given(out[1])), j.d, at_(given(out[2])), j.ldg, at_as<float>(given(out[3])), at_as<float>(given(out[4])),
-        at_(&ws), bytes, stream_of(j.dev));
+    const poet_status s = unlocked([&] {
+      out[0] = fresh({j.T, j.d}, j.type, *j.h);
+      out[1] = fresh({j.T, j.d}, j.type, *j.h);
+      if (j.gate) out[2] = fresh(j.gate->sizes(), j.type, *j.h);
+      if (j.w_post) out[3] = fresh({j.d}, at::kFloat, *j.h);
+      if (j.w_pre) out[4] = fresh({j.d}, at::kFloat, *j.h);
+      const size_t bytes = poet_joint_workspace_bytes(&j.J, j.T);
+      const Tensor ws = fresh({int64_t(bytes ? bytes : 1)}, at::kByte, *j.h);
+      return poet_joint_backward(&j.J, at_(j.o), j.d, at_(j.h), j.d, at_(j.gate), j.ldg, at_(dh_out), j.d, at_(dn), j.d, j.T,
+                                 at_(given(out[0])), j.d, at_(given(out[1])), j.d, at_(given(out[2])), j.ldg,
+                                 at_as<float>(given(out[3])), at_as<float>(given(out[4])), at_(&ws), bytes,
+                                 stream_of(j.dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
@@ -214,18 +230,20 @@ PyObject *token_logprobs(PyObject *, Args a, Py_ssize_t n) {
     const float scale = float(PyFloat_AsDouble(a[3]));
     if (PyErr_Occurred()) return nullptr;
     if (!per_row(tokens, at::kInt, dev, T) || topk < 0 || topk > INT32_MAX) Py_RETURN_NONE;
+    const bool entropy = PyObject_IsTrue(a[4]) == 1;
     std::optional<Tensor> out[5];  // logp, entropy, top_tokens, top_logp, saved
-    if (tokens) out[0] = fresh({T}, at::kFloat, *x);
-    if (PyObject_IsTrue(a[4]) == 1) out[1] = fresh({T}, at::kFloat, *x);
-    if (topk > 0) {
-      out[2] = fresh({T, topk}, at::kInt, *x);
-      out[3] = fresh({T, topk}, at::kFloat, *x);
-    }
-    out[4] = fresh({T, 4}, at::kFloat, *x);
-    const poet_status s = poet_token_logprobs(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
-                                              int32_t(topk), at_as<float>(given(out[0])), at_as<float>(given(out[1])),
-                                              at_as<int32_t>(given(out[2])), at_as<float>(given(out[3])),
-                                              at_as<float>(given(out[4])), stream_of(dev));
+    const poet_status s = unlocked([&] {
+      if (tokens) out[0] = fresh({T}, at::kFloat, *x);
+      if (entropy) out[1] = fresh({T}, at::kFloat, *x);
+      if (topk > 0) {
+        out[2] = fresh({T, topk}, at::kInt, *x);
+        out[3] = fresh({T, topk}, at::kFloat, *x);
+      }
+      out[4] = fresh({T, 4}, at::kFloat, *x);
+      return poet_token_logprobs(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens), int32_t(topk),
+                                 at_as<float>(given(out[0])), at_as<float>(given(out[1])), at_as<int32_t>(given(out[2])),
+                                 at_as<float>(given(out[3])), at_as<float>(given(out[4])), stream_of(dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
@@ -244,10 +262,13 @@ PyObject *token_logprobs_grad(PyObject *, Args a, Py_ssize_t n) {
     if (!per_row(tokens, at::kInt, dev, T) || !plain2(*saved, at::kFloat, dev, T, 4) || !per_row(dlogp, at::kFloat, dev, T) ||
         !per_row(dentropy, at::kFloat, dev, T))
       Py_RETURN_NONE;
-    const std::optional<Tensor> out = fresh({T, V}, x->scalar_type(), *x);
-    const poet_status s = poet_token_logprobs_grad(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
-                                                   at_as<float>(saved), at_as<float>(dlogp), at_as<float>(dentropy),
-                                                   at_(given(out)), V, stream_of(dev));
+    std::optional<Tensor> out;
+    const poet_status s = unlocked([&] {
+      out = fresh({T, V}, x->scalar_type(), *x);
+      return poet_token_logprobs_grad(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
+                                      at_as<float>(saved), at_as<float>(dlogp), at_as<float>(dentropy), at_(given(out)), V,
+                                      stream_of(dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
@@ -272,13 +293,14 @@ PyObject *distill_topk(PyObject *, Args a, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     if (K < 0 || !per_row(dloss, at::kFloat, dev, T)) Py_RETURN_NONE;
     std::optional<Tensor> out[3];  // loss, dlogits, saved
-    out[0] = fresh({T}, at::kFloat, *x);
-    if (grad == 1) out[1] = fresh({T, V}, x->scalar_type(), *x);
-    out[2] = fresh({T, 4}, at::kFloat, *x);
-    const poet_status s = poet_distill_topk(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
-                                            at_as<float>(values), int32_t(K), value_scale, tail == 1, at_as<float>(dloss),
-                                            at_as<float>(given(out[0])), at_as<float>(given(out[2])), at_(given(out[1])), V,
-                                            stream_of(dev));
+    const poet_status s = unlocked([&] {
+      out[0] = fresh({T}, at::kFloat, *x);
+      if (grad == 1) out[1] = fresh({T, V}, x->scalar_type(), *x);
+      out[2] = fresh({T, 4}, at::kFloat, *x);
+      return poet_distill_topk(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens), at_as<float>(values),
+                               int32_t(K), value_scale, tail == 1, at_as<float>(dloss), at_as<float>(given(out[0])),
+                               at_as<float>(given(out[2])), at_(given(out[1])), V, stream_of(dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
@@ -296,10 +318,13 @@ PyObject *distill_topk_grad(PyObject *, Args a, Py_ssize_t n) {
     const int tail = PyObject_IsTrue(a[4]);
     if (PyErr_Occurred()) return nullptr;
     if (K < 0 || !plain2(*saved, at::kFloat, dev, T, 4) || !per_row(dloss, at::kFloat, dev, T)) Py_RETURN_NONE;
-    const std::optional<Tensor> out = fresh({T, V}, x->scalar_type(), *x);
-    const poet_status s = poet_distill_topk_grad(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
-                                                 at_as<float>(values), int32_t(K), value_scale, tail == 1,
-                                                 at_as<float>(saved), at_as<float>(dloss), at_(given(out)), V, stream_of(dev));
+    std::optional<Tensor> out;
+    const poet_status s = unlocked([&] {
+      out = fresh({T, V}, x->scalar_type(), *x);
+      return poet_distill_topk_grad(at_(x), V, dtype_of(*x), T, int32_t(V), scale, at_as<int32_t>(tokens),
+                                    at_as<float>(values), int32_t(K), value_scale, tail == 1, at_as<float>(saved),
+                                    at_as<float>(dloss), at_(given(out)), V, stream_of(dev));
+    });
     return s == POET_OK ? wrap(out) : status(s);
   });
 }
