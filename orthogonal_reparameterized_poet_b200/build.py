@@ -76,7 +76,7 @@ def _binding(force):
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in include], src,
            "-o", path, f"-L{PKG}", "-l:libpoet.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python"]
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{r.stdout}\n{r.stderr}")

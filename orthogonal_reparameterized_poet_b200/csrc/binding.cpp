@@ -11,7 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -59,8 +59,9 @@ template <typename T>
 T *at_as(const Tensor *t) { return static_cast<T *>(at_(t)); }
 poet_stream stream_of(int dev) { return reinterpret_cast<poet_stream>(c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(dev)).stream()); }
 
+// On near's device, without torch's dispatch, which takes longer than the allocation.
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor &near) {
-  return at::empty(shape, near.options().dtype(type).requires_grad(false));
+  return Tensor(at::detail::empty_cuda(shape, type, near.device(), std::nullopt));
 }
 PyObject *wrap(const std::optional<Tensor> &t) {
   if (t) return THPVariable_Wrap(*t);
