@@ -1303,7 +1303,7 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
   for (int i = 0; i < Q; ++i) {
     t[i] = e.t[i];
     xs[i] = e.x[i];
-    lq[i] = e.v[i] * a.value_scale;
+    lq[i] = e.v[i];
     if (t[i] >= a.V && report) atomicOr(a.errword, unsigned(ERR_BOUNDS));
     if (t[i] < 0 || t[i] >= a.V) {
       t[i] = -1;
@@ -1321,13 +1321,14 @@ __device__ __forceinline__ void load_teacher(Teacher &S, const DistillArgs &a, c
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     q[i] = 0.f;
-    if (32 * i < a.K && t[i] >= 0) q[i] = expf(lq[i] - mx);
+    lq[i] = (lq[i] - mx) * a.value_scale;  // the difference first: the products alone may overflow
+    if (32 * i < a.K && t[i] >= 0) q[i] = expf(lq[i]);
     s += q[i];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (!a.tail && s == 0.f) n = 0;  // nothing but -inf: no teacher
-  const float ls = a.tail ? 0.f : mx + logf(s), inv_s = n ? 1.f / s : 0.f;
+  const float ls = a.tail ? 0.f : logf(s), inv_s = n ? 1.f / s : 0.f;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int k = lane + 32 * i;
@@ -1445,7 +1446,7 @@ struct HasTeacher {
     bool any = false;
 #pragma unroll
     for (int i = 0; i < Entries::Q; ++i)
-      any = any || (e.t[i] >= 0 && e.t[i] < a.V && (a.tail || e.v[i] * a.value_scale != -INFINITY));
+      any = any || (e.t[i] >= 0 && e.t[i] < a.V && (a.tail || e.v[i] != -INFINITY));
     return __any_sync(0xffffffffu, any);
   }
 };

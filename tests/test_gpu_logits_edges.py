@@ -145,3 +145,23 @@ def test_without_entropy(torch, T, V, K, kind, dtype):  # noqa: F811
         g = np.take_along_axis(gap, np.maximum(want_top, 0).astype(np.int64), 1)
         with np.errstate(invalid="ignore"):
             _within("top_logp", _np(topl), want_topl, (N + 3 * g + 2 * np.where(finite, np.abs(want_topl), 0) + 2 * lse) * U)
+
+
+@pytest.mark.parametrize("K", [1, 5, 64])
+@pytest.mark.parametrize("value_scale", [1e-37, 1e20, 3.4e38])
+def test_extreme_scales_of_the_teacher(torch, K, value_scale):  # noqa: F811
+    """Up to the largest float: all the mass on the teacher's largest values, also where their products overflow."""
+    x, r = _make(torch, 6, 900, torch.float32)
+    tokens, values = _teacher_case(r, 6, 900, K, False)
+    values[0] = 2.0  # all equal
+    values[1] = -3.0
+    if K > 1:
+        values[2, 0] = values[2, 1] = 9.0  # two of them
+        values[3, 1] = -INF
+        tokens[4, 0] = -1
+    loss, d = _check_distill(torch, x, tokens, values, r, False, 1.0, value_scale, weights=False)
+    # q is 0 or a whole number's inverse, off by K half steps; ln p and p as ever
+    want, dwant, mag = G.distill(_np(x), tokens, values.astype(float), None, float(np.float32(value_scale)))
+    bound = (2 * _steps(900) + 6 * (_gap(_np(x), 1.0).max() + np.log(900)) + 64 + K) * U
+    _within("loss", _np(loss), want, bound * (1 + np.abs(want)))
+    _within("dlogits", _np(d), dwant, bound * mag + 1e-36)
