@@ -1,6 +1,7 @@
 """The joint at the edges of what it accepts, against the float64 oracle
 (oracle/joint.py), with the bounds of tests/test_gpu_joint.py."""
-import numpy as np
+import ctypes
+
 import pytest
 
 from oracle import joint as J
@@ -75,3 +76,53 @@ def test_one_gate_for_any_number_of_tokens(torch, gate):  # noqa: F811
         got.append((out, rec))
     assert all(torch.equal(a, b) for a, b in zip(got[0][0], got[1][0]))
     assert got[0][1] == got[1][1] and got[0][1]["joint"][0] == 1
+
+
+def test_large_offsets(torch):  # noqa: F811
+    """Rows beyond 2^31 elements from the first one."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    d, far = 264, (1 << 30) + 8
+    near = _case(torch, 3, d, torch.bfloat16, "channel", True, 1)
+    buf = torch.empty(4, 3, far, dtype=torch.bfloat16, device="cuda")  # 26 GB
+    o, h, dh, n = (b[:, :d] for b in buf)
+    for v, name in ((o, "o"), (h, "h"), (dh, "dh_out"), (n, "dn")):
+        v.copy_(near[name])
+    h0, n0 = poet.joint_forward(near["o"], near["h"], near["gate"], **near["kw"])
+    want = poet.joint_backward(near["o"], h0, near["gate"], near["dh_out"], near["dn"], **near["kw"])
+    h1, n1 = poet.joint_forward(o, h, near["gate"], **near["kw"], h_out=h)
+    assert h1 is h and torch.equal(h, h0) and torch.equal(n1, n0)
+    got = poet.joint_backward(o, h, near["gate"], dh, n, **near["kw"], dh=dh, d_o=o)
+    poet.poet_sync_status()
+    assert got[0] is dh and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows", [1, 4, 50])
+def test_row_gates_of_any_stride(torch, rows):  # noqa: F811
+    """Through the C ABI: the gate's values a column of a matrix, its gradient a column of another."""
+    from orthogonal_reparameterized_poet_b200 import poet
+
+    T, d = 50, 96
+    c = _case(torch, T, d, torch.float32, "row", True, rows)
+    G = c["gate"].numel()
+    h0, n0 = poet.joint_forward(c["o"], c["h"], c["gate"], **c["kw"])
+    want = poet.joint_backward(c["o"], h0, c["gate"], c["dh_out"], c["dn"], **c["kw"])
+    wide, dwide = torch.full((G, 3), 7.0, device="cuda"), torch.full((G, 5), 7.0, device="cuda")
+    wide[:, 1] = c["gate"]
+    J_ = poet.poet_joint(d, poet.F32, 1, poet.GATE_ROW, poet.GATE_SIGMOID, 0, rows, c["kw"]["alpha"], c["kw"]["beta"], 1e-6,
+                         c["kw"]["w_post"].data_ptr(), c["kw"]["w_pre"].data_ptr())
+    h, n, dh, d_o = (torch.empty_like(h0) for _ in range(4))
+    dwq, dwn = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    ws = torch.empty(poet.joint_workspace_bytes(T, d, poet.F32, poet.GATE_ROW, rows), dtype=torch.uint8, device="cuda")
+    at = lambda t: t.data_ptr()  # noqa: E731
+    st = torch.cuda.current_stream().cuda_stream
+    L, ref = poet.lib(), ctypes.byref(J_)
+    assert L.poet_joint_forward(ref, at(c["o"]), d, at(c["h"]), d, at(wide) + 4, 3, T, at(h), d, at(n), d, st) == poet.OK
+    assert L.poet_joint_backward(ref, at(c["o"]), d, at(h), d, at(wide) + 4, 3, at(c["dh_out"]), d, at(c["dn"]), d, T,
+                                 at(dh), d, at(d_o), d, at(dwide) + 8, 5, at(dwq), at(dwn), at(ws), ws.nbytes, st) == poet.OK
+    poet.poet_sync_status()
+    assert torch.equal(h, h0) and torch.equal(n, n0)
+    for a, b in zip((dh, d_o, dwide[:, 2], dwq, dwn), want):
+        assert torch.equal(a, b)
+    dwide[:, 2] = 7.0
+    assert (dwide == 7.0).all()  # what lies between its values is left as it was
