@@ -841,15 +841,24 @@ poet_status launch_joint(const A &a, const RowShape &s, int64_t groups, size_t s
 
 // Rows of one 16-byte vector per thread go through the ring: four stages up to
 // 512 threads (three in the backward with 257 to 320, where two CTAs share an
-// SM), two up to 1024 (four would not fit).  Wider rows, and rows that do not
-// start on 16 bytes, are read directly.
+// SM); up to 1024, where four would not fit, three in the forward and two in the
+// backward, which has more operands.  Wider rows, and rows that do not start on 16
+// bytes, are read directly.  Measured (us on the GPU, 256 MB an operand, no gate;
+// floors 164 and 245):
+//   forward of 2560 bf16 (320 threads): four stages 264, two CTAs of two 322, direct 483
+//           of 4096 bf16 209, 267, 384; of 2048 float 191, 236, 376
+//           of 5120 bf16 (640 threads): three stages 231, two 369, direct 396
+//           of 8192 bf16 243, 336, 379; of 4096 float 195, 318, 317
+//   backward of 4096 bf16: four stages 405, two 567, direct 515; of 2048 float 314, 482, 453
+//           of 5120 bf16: two stages 743, direct 902; of 8192 771, 772 (a gate each: 1245, 1046)
+//           of 4096 float 569, 665
 template <typename T, int VW, int GK>
 poet_status launch_fwd(const JointFwdArgs &a, const RowShape &s, int64_t groups, int operands, cudaStream_t st) {
   const size_t stage = size_t(s.threads) * 16 * operands;
   if (s.nv == 1) {
     if (s.threads <= 256) return launch_joint<joint_fwd_kernel<T, VW, 1, 4, GK, 256, 3>>(a, s, groups, 4 * stage, st, "joint");
     if (s.threads <= 512) return launch_joint<joint_fwd_kernel<T, VW, 1, 4, GK, 512, 1>>(a, s, groups, 4 * stage, st, "joint");
-    return launch_joint<joint_fwd_kernel<T, VW, 1, 2, GK, 1024, 1>>(a, s, groups, 2 * stage, st, "joint");
+    return launch_joint<joint_fwd_kernel<T, VW, 1, 3, GK, 1024, 1>>(a, s, groups, 3 * stage, st, "joint");
   }
   if (s.nv == 2) return launch_joint<joint_fwd_kernel<T, VW, 2, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
   return launch_joint<joint_fwd_kernel<T, VW, 4, 0, GK, 1024, 1>>(a, s, groups, 0, st, "joint");
