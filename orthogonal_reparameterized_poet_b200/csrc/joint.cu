@@ -51,11 +51,11 @@ struct JointFwdArgs {
 };
 
 // The sigmoid is r = 1 / (1 + e) with e = exp(-g), its slope e r^2: r (1 - r)
-// would lose its digits as the gate opens (r rounds to 1 from g = 17 on).  For
-// bf16 operands the exponential and the reciprocal are the hardware's: their
-// relative error, about 2^-23 (2 + |g|), stays below the rounding of a bf16
-// result, 2^-9, for every gate whose slope is not 0 in float.  For float operands
-// they are CUDA's functions, to a unit or two in the last place.
+// would lose its digits as the gate opens (r rounds to 1 from g = 17 on).  The
+// reciprocal is the hardware's, off by a unit in the last place.  So is the
+// exponential for bf16 operands: its relative error, about 2^-23 (2 + |g|), stays
+// below the rounding of a bf16 result, 2^-9, for every gate whose slope is not 0
+// in float.  For float operands it is CUDA's function, off by two units at most.
 template <typename T>
 __device__ __forceinline__ float exp_minus(float g) {
   if constexpr (sizeof(T) == 4) return expf(-g);
@@ -63,9 +63,7 @@ __device__ __forceinline__ float exp_minus(float g) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
   return e;
 }
-template <typename T>
 __device__ __forceinline__ float sigmoid_of(float e) {
-  if constexpr (sizeof(T) == 4) return __frcp_rn(1.f + e);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
@@ -74,10 +72,7 @@ template <typename T>
 __device__ __forceinline__ float2 exp_minus(float2 g) {
   return make_float2(exp_minus<T>(g.x), exp_minus<T>(g.y));
 }
-template <typename T>
-__device__ __forceinline__ float2 sigmoid_of(float2 e) {
-  return make_float2(sigmoid_of<T>(e.x), sigmoid_of<T>(e.y));
-}
+__device__ __forceinline__ float2 sigmoid_of(float2 e) { return make_float2(sigmoid_of(e.x), sigmoid_of(e.y)); }
 // e r is 1 - r, between 0 and 1; infinity times 0, of a closed gate, saturates to
 // 0 (a NaN's slope is still one: r is).
 __device__ __forceinline__ float2 slope_of(float2 e, float2 r) {
@@ -85,7 +80,7 @@ __device__ __forceinline__ float2 slope_of(float2 e, float2 r) {
 }
 template <typename T>
 __device__ __forceinline__ float act_of(float g, int sig) {
-  return sig ? sigmoid_of<T>(exp_minus<T>(g)) : g;
+  return sig ? sigmoid_of(exp_minus<T>(g)) : g;
 }
 
 // A thread's own ring of the rows to come.  With S stages every thread copies
@@ -364,7 +359,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_fwd_kernel(const JointFwdArg
         vg.get(gv);
         if (a.gate_sigmoid) {
 #pragma unroll
-          for (int p = 0; p < NP; ++p) gv[p] = sigmoid_of<T>(exp_minus<T>(gv[p]));
+          for (int p = 0; p < NP; ++p) gv[p] = sigmoid_of(exp_minus<T>(gv[p]));
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) q[p] = mul2(q[p], gv[p]);
@@ -574,7 +569,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
       if (!SHARED) {
         ga_row = to_float(gate[grow * a.ldg]);
         if (a.gate_sigmoid) {
-          const float2 e = both(exp_minus<T>(ga_row)), r = both(sigmoid_of<T>(e.x));
+          const float2 e = both(exp_minus<T>(ga_row)), r = both(sigmoid_of(e.x));
           ga_row = r.x;
           sl_row = slope_of(e, r).x;
         }
@@ -639,7 +634,7 @@ __global__ void __launch_bounds__(MAXT, MINB) joint_bwd_kernel(const JointBwdArg
           ga = dg[p];
           if (a.gate_sigmoid) {
             const float2 e = exp_minus<T>(ga);
-            ga = sigmoid_of<T>(e);
+            ga = sigmoid_of(e);
             sl = slope_of(e, ga);
           }
         }
