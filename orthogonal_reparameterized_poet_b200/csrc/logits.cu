@@ -1814,12 +1814,21 @@ poet_status launch_rows(const A &a, const Spread &s, int threads, cudaStream_t s
   return launch_status(what);
 }
 
-// Columns up to which two warps work on a row.  NARROW, and MEDIUM bytes up to
-// which four do in a distillation: more rows at once hide more of what comes
-// between a row's two passes.  Measured (us, four warps / eight): 8192 rows of
-// 32000 bf16 238 / 252, 1000 of 50257 56 / 63, 2048 of 64000 132 / 119, 2048 of
-// 128000 270 / 260.
-constexpr int NARROW = 8192, MEDIUM = 112 * 1024;
+// How many warps work on a row, by its bytes: fewer of them let more rows share an
+// SM, which hides what comes between a row's passes, and more read a long row
+// faster.  Measured (us on the GPU, 512 MB of logits, two / four / eight warps):
+//   loss and gradient, bf16: rows of 4096 467 / 470 / 749, of 6000 420 / 425 / 526, of 7000 422 / 379 / 467, of
+//     50257 285 / 232 / 247, of 56000 276 / 257 / 229, of 128000 301 / 281 / 268
+//   float: of 3000 313 / 340 / 470, of 4096 265 / 255 / 336, of 8192 221 / 190 / 218, of 15000 223 / 186 / 187, of
+//     16000 237 / 209 / 181, of 28000 272 / 247 / 195
+//   log probabilities without alternatives, bf16: of 6000 152 / 173 / 197, of 7000 163 / 150 / 170, of 12000 134 /
+//     119 / 152, of 28000 119 / 105 / 113, of 32000 121 / 103 / 101, of 128000 114 / 101 / 95
+//   float: of 3000 114 / 136 / 164, of 4096 101 / 97 / 115, of 8192 88 / 91 / 86, of 16000 97 / 92 / 89
+// The loss alone takes the warps of the loss with its gradient, and so its bits.
+constexpr int64_t KB = 1024, NARROW = 13 * KB, LOGP_FOUR = 56 * KB, ALTERNATIVES_FOUR = 112 * KB;
+template <typename T>
+constexpr int64_t DISTILL_FOUR = (sizeof(T) == 2 ? 104 : 60) * KB;
+constexpr int NARROW_SELECT = 8192;  // columns, with alternatives
 
 template <typename T, int NW>
 poet_status run_logp(LogpArgs &a, int cluster, cudaStream_t st) {
@@ -1844,14 +1853,16 @@ poet_status run_logp(LogpArgs &a, cudaStream_t st) {
   // A selection takes as long for short rows as for long ones, so with few alternatives more and smaller CTAs share
   // an SM; many need the maxima of many threads.  Measured with four warps / eight (us): 8192 rows of 32000 bf16
   // with 20 142 / 192, with 64 232 / 248; 4096 of 64000 with 20 117 / 127, with 64 173 / 161; 4096 of 128000 with
-  // 64 232 / 223, without 172 / 170; 16384 of 32000 without 194 / 189; with two / eight: 16384 of 8000 with 20
-  // 155 / 313.
+  // 64 232 / 223; of float 5592 of 24000 with 64 157 / 169, 4194 of 32000 159 / 146.  With two / four warps and 20:
+  // bf16 44739 of 6000 372 / 460, 32768 of 8192 295 / 337, 22369 of 12000 233 / 256 but 400 of 12000 12.9 / 11.0; float
+  // 16384 of 8192 151 / 170, 400 of 12000 14.9 / 13.0; with 64, 32768 of 8192 973 / 603.
   // With a row an SM at most there is nothing to share and eight warps are the quickest (two or four / eight on the
   // GPU, with 20: 4 rows of 8000 8.2 / 7.4, of 32000 10.6 / 9.4, of 128000 14.8 / 12.2; of 1000, where eight warps
   // have no logits for every thread, 6.6 / 13.7).
   if (a.K && a.T <= num_sms() && a.V >= 4096) return run_logp<T, 8>(a, cluster, st);
-  if (a.V <= NARROW && a.K <= 32) return run_logp<T, 2>(a, cluster, st);
-  if (a.K && (a.K <= 32 || (a.K <= 64 && int64_t(a.V) * int64_t(sizeof(T)) <= MEDIUM)))
+  const int64_t bytes = int64_t(a.V) * int64_t(sizeof(T));
+  if (a.K ? a.V <= NARROW_SELECT && a.K <= 32 : bytes <= NARROW) return run_logp<T, 2>(a, cluster, st);
+  if (a.K ? a.K <= 32 || (a.K <= 64 && bytes <= ALTERNATIVES_FOUR) : bytes <= LOGP_FOUR)
     return run_logp<T, 4>(a, cluster, st);
   return run_logp<T, 8>(a, cluster, st);
 }
@@ -1868,8 +1879,9 @@ poet_status run_distill(DistillArgs &a, int cluster, cudaStream_t st) {
 template <typename T>
 poet_status run_distill(DistillArgs &a, cudaStream_t st) {
   const int cluster = cluster_of(a.T, a.V);
-  if (a.V <= NARROW) return run_distill<T, 2>(a, cluster, st);
-  return int64_t(a.V) * int64_t(sizeof(T)) <= MEDIUM ? run_distill<T, 4>(a, cluster, st) : run_distill<T, 8>(a, cluster, st);
+  const int64_t bytes = int64_t(a.V) * int64_t(sizeof(T));
+  if (bytes <= NARROW) return run_distill<T, 2>(a, cluster, st);
+  return bytes <= DISTILL_FOUR<T> ? run_distill<T, 4>(a, cluster, st) : run_distill<T, 8>(a, cluster, st);
 }
 
 poet_status check_teacher(const char *what, const int32_t *tokens, const float *values, int32_t K, float value_scale,
