@@ -80,9 +80,6 @@ def _binding(force):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{r.stdout}\n{r.stderr}")
-    for other in glob.glob(os.path.join(PKG, "_binding*.so")):  # of another torch or interpreter
-        if other != path:
-            os.remove(other)
 
 
 def _binding_if_possible(force):

@@ -20,11 +20,12 @@
 // backward from the rows it reads anyway, which costs no traffic and saves a
 // buffer.
 //
-// Measured (bf16): forward of 32768 x 2048 95 us, 5.65 TB/s of a copy's 6.56;
-// backward 193 us of 805 MB, of 16384 x 2560 with a gate each 145 us of 671 MB.
-// What bounds the backward now is instruction issue (about 500 instructions for a
-// warp's 256 elements of a row; 60 % of the slots are used) with the registers
-// for two rows an SM at once.  Tried and slower: three CTAs an SM (spills, 276
+// Measured (bf16, on the GPU): forward of 32768 x 2048 92 us, 5.8 TB/s of a copy's
+// 6.56; backward 193 us of 805 MB, of 16384 x 2560 with a gate each 145 us of 671
+// MB (a call among others 92 to 96 and 145 to 150).  What bounds the backward is
+// latency: no unit is saturated (issue slots 60 %, DRAM 47 %), a warp has about 500
+// instructions for its 256 elements of a row, and registers and shared memory leave
+// room for two rows an SM at once.  Tried and slower: three CTAs an SM (spills, 276
 // us), the gains in registers with 320 threads (spills, 324 us against 164).
 #include <cmath>
 

@@ -13,16 +13,20 @@
 // CTAs, each with a contiguous slice) works through rows, and one warp of it
 // streams their 16-byte vectors through a ring of stages in shared memory by
 // bulk copies, so that the next rows are on their way while a row's sums are
-// joined, its alternatives selected or its gradient written.  What bounds them:
-// HBM (each logit is read once, each gradient written once) and, close behind,
-// the exponential (16 a clock and SM: for a bf16 logit 73 % of the time that HBM
-// needs) and instruction issue, hence the arithmetic in pairs.
+// joined, its alternatives selected or its gradient written.  What they cannot go
+// below: HBM (each logit is read once, each gradient written once) and, close
+// behind, the exponential (16 a clock and SM: for a bf16 logit 73 % of the time
+// that HBM needs) and instruction issue, hence the arithmetic in pairs.  None of
+// them is saturated (issue slots 57 to 65 %, exponentials 51 to 63 %, DRAM 47 to
+// 61 % of nominal): a row's join, and the second reading, from L2, of a row that
+// does not fit the ring when its gradient is wanted, are not hidden entirely.
 //
-// Measured (bf16, of a copy's 6.56 TB/s): log probabilities and entropy of 4096
-// rows of 128000 170 us (6.2 TB/s), of 16384 of 32000 189 us (5.5; the stream
-// without the arithmetic 156 us); with 64 alternatives of 4096 x 128000 225 us;
-// loss and gradient of 8192 x 32000 240 us (4.4: two exponentials a logit, a
-// join between the passes), the gradient alone from saved sums 6.4.  Tried and
+// Measured (bf16, on the GPU, every row live, of a copy's 6.56 TB/s): log
+// probabilities and entropy of 4096 rows of 128000 170 us (6.2 TB/s), of 16384 of
+// 32000 191 us (5.5; the stream without the arithmetic 156 us); with 64
+// alternatives of 4096 x 128000 223 us; loss and gradient of 8192 x 32000 239 us
+// (4.4), the loss alone 119, the gradient alone from saved sums 6.4 TB/s.  A call
+// among others takes up to 7 % more, depending on the machine.  Tried and
 // slower: a quarter of the exponentials by a polynomial (217 us against 197, issue
 // and FMA bound), a cluster for rows that do not fit a CTA's ring (80 us against
 // 64, the exchange of every row), the two passes of a loss with its gradient in
@@ -50,6 +54,10 @@ constexpr float LOWEST = -1e30f;
 // scale log2(e), finite: an infinite one would make NaN of a difference of 0.
 __device__ __forceinline__ float log2_scale(float scale) { return fminf(scale * LOG2E, 3.4028234e38f); }
 
+// The hardware's exponential, off by two units in the last place, and 0 below
+// 2^-126, where a probability counts for nothing beside the row's largest.  With the
+// rounding of its argument a probability p is off by about 2^-23 (2 + |ln p|) of
+// itself; CUDA's own function has the argument's error too.
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
